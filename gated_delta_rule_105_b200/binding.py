@@ -15,7 +15,7 @@ _PKG = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_PKG, "libgdn.so")
 
 GDN_OK, GDN_ERR_INVALID_ARG, GDN_ERR_UNSUPPORTED, GDN_ERR_CUDA, GDN_ERR_TIMEOUT, GDN_ERR_DEVICE_ARG = range(6)
-GDN_F32, GDN_BF16 = 0, 1
+GDN_F32, GDN_BF16, GDN_E4M3 = 0, 1, 2
 KERNELS = {"auto": 0, "simt": 1, "tc": 2}
 KERNEL_NAMES = {v: k for k, v in KERNELS.items()}
 
@@ -85,6 +85,21 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.gdn2_chunk_bwd.restype = i
     lib.gdn_kda_chunk_bwd.argtypes = [vp, vp, vp, fp, fp, f, fp, vp, fp] + [fp] * 6 + [i] * 6 + [i, vp, i, vp, sz, vp]
     lib.gdn_kda_chunk_bwd.restype = i
+    ll = ctypes.c_longlong
+    lib.gdn_kv_append.argtypes = [vp, vp, ll, ll] + [vp] * 7 + [i] * 9 + [vp]
+    lib.gdn_kv_append.restype = i
+    lib.gdn_kv_read.argtypes = [vp] * 8 + [i] * 9 + [vp]
+    lib.gdn_kv_read.restype = i
+    lib.gdn_paged_attn_workspace_bytes.argtypes = [i] * 5
+    lib.gdn_paged_attn_workspace_bytes.restype = sz
+    lib.gdn_paged_attn_fwd.argtypes = [vp, ll] + [vp] * 7 + [f, i, vp, vp] + [i] * 10 + [vp, sz, vp]
+    lib.gdn_paged_attn_fwd.restype = i
+    lib.gdn_add_rmsnorm_fwd.argtypes = [vp] * 7 + [ll, i, i, i, i, f, vp]
+    lib.gdn_add_rmsnorm_fwd.restype = i
+    lib.gdn_add_rmsnorm_bwd_workspace_bytes.argtypes = [ll, i]
+    lib.gdn_add_rmsnorm_bwd_workspace_bytes.restype = sz
+    lib.gdn_add_rmsnorm_bwd.argtypes = [vp] * 7 + [ll, i, i, vp, sz, vp]
+    lib.gdn_add_rmsnorm_bwd.restype = i
     lib.gdn_debug_stall.argtypes = [i]
     lib.gdn_debug_stall.restype = i
     _lib = lib
@@ -143,7 +158,9 @@ def check_error(stream=None) -> None:
 
 PROFILE_KERNELS = {"gdn_simt_fwd_kernel": 0, "gdn_tc_wy_kernel": 1, "gdn_tc_fwd_kernel": 2, "gdn2_tc_prep_kernel": 3,
                    "gdn2_tc_fwd_kernel": 4, "gdn_decode_kernel": 5, "gdn_prelude_kernel": 6,
-                   "gdn_output_gate_kernel": 7, "gdn_bwd_kernels": 8}
+                   "gdn_output_gate_kernel": 7, "gdn_bwd_kernels": 8, "gdn_kv_append_kernel": 16,
+                   "gdn_kv_read_kernel": 17, "gdn_paged_attn_kernels": 18, "gdn_add_rmsnorm_kernel": 19,
+                   "gdn_add_rmsnorm_bwd_kernels": 20}
 
 
 def profile_enable(on: bool = True) -> None:
@@ -521,3 +538,259 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, d_o, scale=None, h0=None, dhT=None, cu_s
     """Backward pass of :func:`gdn_kda_chunk_fwd` through ``gdn_kda_chunk_bwd``.  g [B,T,H,dk] and beta [B,T,H]
     fp32.  Returns fp32 dq, dk, dv, dg [B,T,H,dk], dbeta [B,T,H] and dh0."""
     return _bwd2(True, q, k, v, g, beta, None, d_o, scale, h0, dhT, cu_seqlens, BT, workspace, want_dh0)
+
+
+# ------------------------------------------------------------------------------------------ the attention layer
+_CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_E4M3}
+
+
+def _addr(t):
+    return None if t is None else t.data_ptr()
+
+
+def _on(dev, *named):
+    """Every tensor of the call lies on one CUDA device (None entries are left out)."""
+    for name, t in named:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be a CUDA tensor on {dev}, like the call's other tensors, got {t.device}")
+
+
+class _Device:
+    """Makes a tensor's device current for the launch (a context manager only where it is not already)."""
+    __slots__ = ("dev", "prev")
+
+    def __init__(self, dev):
+        if dev.type != "cuda":
+            raise ValueError("the tensors must be CUDA tensors (libgdn has no CPU path)")
+        self.dev = dev
+
+    def __enter__(self):
+        cur = torch.cuda.current_device()
+        self.prev = None if self.dev.index == cur else cur
+        if self.prev is not None:
+            torch.cuda.set_device(self.dev)
+        return torch.cuda.current_stream(self.dev).cuda_stream
+
+    def __exit__(self, *exc):
+        if self.prev is not None:
+            torch.cuda.set_device(self.prev)
+        return False
+
+
+def _rows(name, t, heads, d):
+    """[n, heads, d] whose tokens may lie apart (a slice of a fused projection): returns the token stride."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
+        raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
+    s0, s1, s2 = t.stride()
+    if s2 != 1 or (heads > 1 and s1 != d):
+        raise ValueError(f"{name}'s heads and channels must be contiguous (only its tokens may lie apart)")
+    return s0 if t.shape[0] > 1 else max(s0, heads * d)
+
+
+def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
+    """Checks of the paged cache; returns (n_pages, Hkv, page_size, d, dtype code, n_seqs, max_pages)."""
+    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must be [n_pages, Hkv, page_size, d] of one shape and dtype")
+    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
+        raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
+    eight = k_cache.dtype is torch.float8_e4m3fn
+    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+        if eight != (t is not None):
+            raise ValueError("k_scale and v_scale go with an 8-bit cache, and only with one")
+        if eight and (t.dtype is not torch.uint8 or t.shape != k_cache.shape[:3]):
+            raise ValueError(f"{name} must be uint8 [n_pages, Hkv, page_size]")
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32:
+        raise ValueError("block_table must be int32 [n_seqs, max_pages]")
+    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+                    ("block_table", block_table)):
+        if t is not None and not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+    n_pages, hkv, page, d = k_cache.shape
+    return n_pages, hkv, page, d, _CODES[k_cache.dtype], block_table.shape[0], block_table.shape[1]
+
+
+def _seq_args(n_seqs, seq_lens, cu_seqlens):
+    for name, t, n in (("seq_lens", seq_lens, n_seqs), ("cu_seqlens", cu_seqlens, n_seqs + 1)):
+        if t is not None and (t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
+            raise ValueError(f"{name} must be a contiguous int32 [{n}]")
+
+
+def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None):
+    """Write new tokens' keys and values into the paged cache (``gdn_kv_append``), in place.
+
+    k, v [n_tok, Hkv, d] fp32 or bf16 (tokens may lie apart); caches [n_pages, Hkv, page_size, d] bf16, or
+    float8_e4m3fn with k_scale, v_scale uint8 [n_pages, Hkv, page_size]; block_table int32 [n_seqs, max_pages];
+    seq_lens int32 [n_seqs] (positions in the cache, these tokens among them); cu_seqlens int32 [n_seqs + 1], or None
+    for n_tok / n_seqs tokens each.  Returns (k_cache, v_cache).
+    """
+    n_pages, hkv, page, d, code, n_seqs, max_pages = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    ks, vs = _rows("k", k, hkv, d), _rows("v", v, hkv, d)
+    if v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError("k and v must have one shape, and be both float32 or both bfloat16")
+    _seq_args(n_seqs, seq_lens, cu_seqlens)
+    dev = k.device
+    _on(dev, ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+        ("block_table", block_table), ("seq_lens", seq_lens), ("cu_seqlens", cu_seqlens))
+    with _Device(dev) as stream:
+        st = load_library().gdn_kv_append(
+            k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+            block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), k.shape[0], n_seqs, n_pages, max_pages,
+            page, hkv, d, _CODES[k.dtype], code, stream)
+    _raise_on(st)
+    return k_cache, v_cache
+
+
+def kv_read(k_cache, v_cache, block_table, cu_seqlens, n_rows, k_scale=None, v_scale=None, dtype=torch.bfloat16,
+            k=None, v=None):
+    """Read the paged cache back as dense rows (``gdn_kv_read``): returns k, v [n_rows, Hkv, d] in ``dtype`` (bf16 or
+    fp32, both exact).  Rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 are positions 0, 1, ... of sequence n; rows behind
+    the last sequence are left as they were (undefined in outputs allocated here)."""
+    n_pages, hkv, page, d, code, n_seqs, max_pages = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    if dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
+    if cu_seqlens is None:
+        raise ValueError("cu_seqlens is required")
+    _seq_args(n_seqs, None, cu_seqlens)
+    dev = k_cache.device
+    k = torch.empty((n_rows, hkv, d), dtype=dtype, device=dev) if k is None else k
+    v = torch.empty((n_rows, hkv, d), dtype=dtype, device=dev) if v is None else v
+    for name, t in (("k", k), ("v", v)):
+        if t.shape != (n_rows, hkv, d) or t.dtype != dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} [{n_rows}, {hkv}, {d}]")
+    _on(dev, ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("block_table", block_table),
+        ("cu_seqlens", cu_seqlens), ("k", k), ("v", v))
+    with _Device(dev) as stream:
+        st = load_library().gdn_kv_read(
+            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
+            cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), n_rows, n_seqs, n_pages, max_pages, page, hkv, d, code,
+            _CODES[dtype], stream)
+    _raise_on(st)
+    return k, v
+
+
+def paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d) -> int:
+    """Device workspace (bytes) ``paged_attn_fwd`` needs for these sizes (a fixed amount per CTA, whatever the
+    sequences' lengths)."""
+    return int(load_library().gdn_paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d))
+
+
+def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None, scale=None,
+                   window=0, o=None, o_dtype=torch.bfloat16, return_lse=False, workspace=None):
+    """Causal attention of new tokens over the paged cache, which holds their keys and values already
+    (``gdn_paged_attn_fwd``): one token per sequence, chunks of prompts, or both in one call.
+
+    q [n_tok, Hq, d] bf16 (tokens may lie apart), Hq a multiple of Hkv; the cache, block_table, seq_lens and
+    cu_seqlens as for :func:`kv_append`; ``window`` > 0 lets a token see its last ``window`` positions only.  Returns
+    o [n_tok, Hq, d] in ``o_dtype`` (bf16 or fp32), with ``return_lse`` also the softmax denominators' natural
+    logarithms [n_tok, Hq] fp32.  ``workspace`` (uint8, at least :func:`paged_attn_workspace_bytes`) is allocated per
+    call when not given."""
+    n_pages, hkv, page, d, code, n_seqs, max_pages = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
+    if q.dim() != 3 or q.dtype is not torch.bfloat16:
+        raise ValueError("q must be bfloat16 [tokens, Hq, d]")
+    n_tok, hq = q.shape[0], q.shape[1]
+    qs = _rows("q", q, hq, d)
+    _seq_args(n_seqs, seq_lens, cu_seqlens)
+    if o_dtype not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"o_dtype must be float32 or bfloat16, got {o_dtype}")
+    dev = q.device
+    with _Device(dev) as stream:
+        if o is None:
+            o = torch.empty((n_tok, hq, d), dtype=o_dtype, device=dev)
+        elif o.shape != (n_tok, hq, d) or o.dtype != o_dtype or not o.is_contiguous():
+            raise ValueError(f"o must be a contiguous {o_dtype} [{n_tok}, {hq}, {d}]")
+        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=dev) if return_lse else None
+        if workspace is None:
+            workspace = torch.empty(paged_attn_workspace_bytes(n_tok, n_seqs, hq, hkv, d), dtype=torch.uint8,
+                                    device=dev)
+        _check_dev("workspace", workspace, torch.uint8)
+        _on(dev, ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
+            ("block_table", block_table), ("seq_lens", seq_lens), ("cu_seqlens", cu_seqlens), ("o", o),
+            ("workspace", workspace))
+        st = load_library().gdn_paged_attn_fwd(
+            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+            block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else scale,
+            window, o.data_ptr(), _addr(lse), n_tok, n_seqs, n_pages, max_pages, page, hq, hkv, d, code,
+            _CODES[o_dtype], workspace.data_ptr(), workspace.numel(), stream)
+    _raise_on(st)
+    return (o, lse) if return_lse else o
+
+
+def add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, s=None):
+    """The residual stream's RMS norm (``gdn_add_rmsnorm_fwd``): s = x + residual, y = s rstd weight over the last axis.
+
+    x, residual [..., d] fp32 or bf16, weight [d] fp32.  ``out_dtype``: x's dtype (default) or float8_e4m3fn, with
+    fp32 scales per row (``group`` 0) or per 128 channels (``group`` 128): value = y * scale.  ``s`` may be given (x or
+    residual itself for an update in place).  Returns a dict: s (x itself without a residual), y, rstd [rows], and
+    scale ([rows, 1] or [rows, d / 128]; None without 8 bits)."""
+    d = x.shape[-1]
+    dt = x.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"x must be float32 or bfloat16, got {dt}")
+    out_dtype = dt if out_dtype is None else out_dtype
+    if out_dtype != dt and out_dtype is not torch.float8_e4m3fn:
+        raise ValueError(f"out_dtype must be x's dtype or float8_e4m3fn, got {out_dtype}")
+    _check_dev("x", x)
+    _check_dev("weight", weight, torch.float32)
+    if weight.shape != (d,):
+        raise ValueError("weight must be [d]")
+    if group not in (0, 128) or (group and (out_dtype == dt or d % group)):
+        raise ValueError("group is 0, or 128 with an 8-bit output and d a multiple of 128")
+    rows = x.numel() // d if d else 0
+    dev = x.device
+    with _Device(dev) as stream:
+        if residual is not None:
+            _check_dev("residual", residual, dt)
+            if residual.shape != x.shape:
+                raise ValueError("residual must have x's shape")
+            s = torch.empty_like(x) if s is None else s
+        if s is not None:
+            _check_dev("s", s, dt)
+            if s.shape != x.shape:
+                raise ValueError("s must have x's shape")
+        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
+        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
+        scale = None
+        if out_dtype != dt:
+            scale = torch.empty((rows, d // group if group else 1), dtype=torch.float32, device=dev)
+        _on(dev, ("weight", weight), ("residual", residual), ("s", s))
+        st = load_library().gdn_add_rmsnorm_fwd(
+            x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(s), y.data_ptr(), _addr(scale), rstd.data_ptr(),
+            rows, d, _CODES[dt], _CODES[out_dtype], group, eps, stream)
+    _raise_on(st)
+    return {"s": x if s is None else s, "y": y, "rstd": rstd, "scale": scale}
+
+
+def add_rmsnorm_bwd_workspace_bytes(rows, d) -> int:
+    """Device workspace (bytes) ``add_rmsnorm_bwd`` needs."""
+    return int(load_library().gdn_add_rmsnorm_bwd_workspace_bytes(rows, d))
+
+
+def add_rmsnorm_bwd(dy, s, weight, rstd, ds=None, dx=None, workspace=None):
+    """Backward pass of :func:`add_rmsnorm_fwd` (``gdn_add_rmsnorm_bwd``): dy the gradient of y, ds (or None) the one
+    that reaches s by the residual path, s and rstd the forward's.  Returns a dict: dx (in s's dtype: the gradient of
+    x and, the same, of residual; may be given, dy or ds itself for an update in place) and dweight [d] fp32."""
+    d, dt = s.shape[-1], s.dtype
+    if dt not in (torch.float32, torch.bfloat16):
+        raise ValueError(f"s must be float32 or bfloat16, got {dt}")
+    for name, t in (("s", s), ("dy", dy), ("ds", ds), ("dx", dx)):
+        _check_dev(name, t, dt)
+        if t is not None and t.shape != s.shape:
+            raise ValueError(f"{name} must have s's shape")
+    rows = s.numel() // d if d else 0
+    _check_dev("weight", weight, torch.float32)
+    _check_dev("rstd", rstd, torch.float32)
+    if weight.shape != (d,) or rstd.numel() != rows:
+        raise ValueError("weight must be [d] and rstd one value per row")
+    dev = s.device
+    with _Device(dev) as stream:
+        dx = torch.empty_like(s) if dx is None else dx
+        dweight = torch.empty(d, dtype=torch.float32, device=dev)
+        if workspace is None:
+            workspace = torch.empty(add_rmsnorm_bwd_workspace_bytes(rows, d), dtype=torch.uint8, device=dev)
+        _check_dev("workspace", workspace, torch.uint8)
+        _on(dev, ("dy", dy), ("ds", ds), ("dx", dx), ("weight", weight), ("rstd", rstd), ("workspace", workspace))
+        st = load_library().gdn_add_rmsnorm_bwd(
+            dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(ds), dx.data_ptr(),
+            dweight.data_ptr(), rows, d, _CODES[dt], workspace.data_ptr() or None, workspace.numel(), stream)
+    _raise_on(st)
+    return {"dx": dx, "dweight": dweight}

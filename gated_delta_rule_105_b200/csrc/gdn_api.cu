@@ -1,5 +1,6 @@
-// libgdn C ABI: host-side argument checks, kernel selection and launches.  Every kernel of the library
-// is included here so that they share one device error word without relocatable device code.
+// libgdn C ABI: host-side argument checks, kernel selection and launches of the token mixer's kernels.  The
+// device error word lives here; the kernels of gdn_attn_api.cu get its address as an argument, so no relocatable
+// device code is needed.
 #include <algorithm>
 #include <atomic>
 #include <cmath>
@@ -10,6 +11,7 @@
 
 #include "gdn.h"
 #include "gdn_common.cuh"
+#include "gdn_host.h"
 #include "gdn_prof.cuh"
 #include "gdn_simt.cuh"
 #include "gdn_tc.cuh"
@@ -41,7 +43,7 @@ constexpr int kMaxDevices = 64;
 static std::atomic<void*> g_static_ws_addr[kMaxDevices];
 static std::mutex g_static_ws_mu;
 
-static gdn_status fail(gdn_status st, const char* fmt, ...) {
+gdn_status fail(gdn_status st, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
     vsnprintf(t_msg, sizeof(t_msg), fmt, ap);
@@ -49,9 +51,9 @@ static gdn_status fail(gdn_status st, const char* fmt, ...) {
     return st;
 }
 
-static bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
+void clear_error() { t_msg[0] = 0; }
 
-static unsigned* err_word_ptr(gdn_status* st) {
+unsigned* err_word_ptr(gdn_status* st) {
     unsigned* ptr = nullptr;
     cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&ptr), g_err_word);
     if (e != cudaSuccess) {
@@ -648,6 +650,8 @@ gdn_status gdn_check_error(cudaStream_t stream) {
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "error word: %s", cudaGetErrorString(e));
     if (word & kErrTimeout) return fail(GDN_ERR_TIMEOUT, "a bounded device wait ran out (word 0x%x)", word);
     if (word & kErrSeqlens) return fail(GDN_ERR_DEVICE_ARG, "cu_seqlens out of order or out of range (word 0x%x)", word);
+    if (word & kErrPages)
+        return fail(GDN_ERR_DEVICE_ARG, "a page index or a sequence length is out of range (word 0x%x)", word);
     return GDN_OK;
 }
 
@@ -658,7 +662,7 @@ const char* gdn_status_string(gdn_status s) {
         case GDN_ERR_UNSUPPORTED: return "unsupported shape or option";
         case GDN_ERR_CUDA: return "CUDA error";
         case GDN_ERR_TIMEOUT: return "device wait timed out";
-        case GDN_ERR_DEVICE_ARG: return "invalid cu_seqlens seen on the device";
+        case GDN_ERR_DEVICE_ARG: return "invalid cu_seqlens, sequence length or page seen on the device";
     }
     return "unknown status";
 }
@@ -672,7 +676,9 @@ gdn_status gdn_profile_enable(int on) {
 
 gdn_status gdn_profile_take(int kernel, int* launches, double* total_ms) {
     t_msg[0] = 0;
-    if (kernel < 0 || kernel >= PK_COUNT) return fail(GDN_ERR_INVALID_ARG, "kernel id must be 0..%d", PK_COUNT - 1);
+    if (kernel < 0 || kernel >= PK_COUNT || (kernel > PK_BWD && kernel < PK_KV_APPEND))
+        return fail(GDN_ERR_INVALID_ARG, "kernel id must be 0..%d or %d..%d", (int)PK_BWD, (int)PK_KV_APPEND,
+                    PK_COUNT - 1);
     if (!launches || !total_ms) return fail(GDN_ERR_INVALID_ARG, "NULL output pointer");
     if (!prof_take(kernel, launches, total_ms)) return fail(GDN_ERR_CUDA, "a recorded launch event failed");
     return GDN_OK;

@@ -1,0 +1,363 @@
+// libgdn C ABI, the attention layer beside the token mixer: the paged key/value cache, attention over it, and the
+// residual stream's RMS norm.  Host-side argument checks and launches.
+#include <algorithm>
+#include <cmath>
+
+#include "gdn.h"
+#include "gdn_attn.cuh"
+#include "gdn_host.h"
+#include "gdn_norm.cuh"
+#include "gdn_prof.cuh"
+
+namespace gdn {
+
+// Launches `kern` so that it may start while the launch before it on the stream still drains (programmatic stream
+// serialisation); the kernel waits for that launch's memory with cudaGridDependencySynchronize().
+template <typename P>
+static cudaError_t launch_after(void (*kern)(P), dim3 grid, dim3 block, cudaStream_t stream, const P& params) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, params);
+}
+
+static gdn_status check_ptrs(std::initializer_list<const void*> required, std::initializer_list<const void*> optional) {
+    for (const void* ptr : required) {
+        if (!ptr) return fail(GDN_ERR_INVALID_ARG, "a required pointer is NULL");
+        if (!aligned16(ptr)) return fail(GDN_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", ptr);
+    }
+    for (const void* ptr : optional)
+        if (ptr && !aligned16(ptr)) return fail(GDN_ERR_INVALID_ARG, "pointer %p is not 16-byte aligned", ptr);
+    return GDN_OK;
+}
+
+// The checks that every call on the paged cache shares; fills the layout.
+static gdn_status check_cache(KvParams* c, const void* k_cache, const void* v_cache, const uint8_t* k_scale,
+                              const uint8_t* v_scale, const int32_t* table, int n_tok, int n_seqs, int n_pages,
+                              int max_pages, int page_size, int Hkv, int d, gdn_dtype cache_dt) {
+    if (n_tok < 0) return fail(GDN_ERR_INVALID_ARG, "the number of tokens must be >= 0 (got %d)", n_tok);
+    if (n_seqs < 1 || n_seqs > 65535) return fail(GDN_ERR_INVALID_ARG, "n_seqs must be in [1, 65535] (got %d)", n_seqs);
+    if (n_pages < 1 || max_pages < 1)
+        return fail(GDN_ERR_INVALID_ARG, "need n_pages >= 1 and max_pages >= 1 (got %d, %d)", n_pages, max_pages);
+    if (page_size != 16 && page_size != 32 && page_size != 64 && page_size != 128)
+        return fail(GDN_ERR_UNSUPPORTED, "page_size must be 16, 32, 64 or 128 (got %d)", page_size);
+    if (Hkv < 1 || Hkv > 1024) return fail(GDN_ERR_INVALID_ARG, "Hkv must be in [1, 1024] (got %d)", Hkv);
+    if (d != 64 && d != 128) return fail(GDN_ERR_UNSUPPORTED, "d must be 64 or 128 (got %d)", d);
+    if (cache_dt != GDN_BF16 && cache_dt != GDN_E4M3)
+        return fail(GDN_ERR_UNSUPPORTED, "the cache is GDN_BF16 or GDN_E4M3 (got %d)", (int)cache_dt);
+    if ((long long)n_pages * Hkv * page_size > 0x7fffffffLL)
+        return fail(GDN_ERR_UNSUPPORTED, "n_pages * Hkv * page_size must be below 2^31");
+    if ((long long)max_pages * page_size > 0x7fffff00LL)
+        return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size must be below 2^31 - 255");
+    gdn_status st = check_ptrs({k_cache, v_cache, table}, {k_scale, v_scale});
+    if (st != GDN_OK) return st;
+    if (cache_dt == GDN_E4M3 && (!k_scale || !v_scale))
+        return fail(GDN_ERR_INVALID_ARG, "an 8-bit cache needs k_scale and v_scale");
+    if (cache_dt == GDN_BF16 && (k_scale || v_scale))
+        return fail(GDN_ERR_INVALID_ARG, "k_scale and v_scale go with an 8-bit cache only");
+    c->k_cache = const_cast<void*>(k_cache);
+    c->v_cache = const_cast<void*>(v_cache);
+    c->k_scale = const_cast<uint8_t*>(k_scale);
+    c->v_scale = const_cast<uint8_t*>(v_scale);
+    c->table = table;
+    c->seq_lens = nullptr;
+    c->cu = nullptr;
+    c->n_tok = n_tok;
+    c->n_seq = n_seqs;
+    c->n_pages = n_pages;
+    c->max_pages = max_pages;
+    c->hkv = Hkv;
+    c->d = d;
+    c->page_log2 = page_size == 16 ? 4 : page_size == 32 ? 5 : page_size == 64 ? 6 : 7;
+    return GDN_OK;
+}
+
+static gdn_status check_stride(const char* what, long long stride, long long width, int esize) {
+    if (stride < width || stride * esize % 16 != 0)
+        return fail(GDN_ERR_INVALID_ARG, "%s must be at least %lld elements and a multiple of 16 bytes (got %lld)", what,
+                    width, stride);
+    return GDN_OK;
+}
+
+template <typename TIn, int D>
+static void launch_append(const KvAppendParams& p, bool e4m3, unsigned grid, unsigned* err, cudaStream_t stream) {
+    if (e4m3) gdn_kv_append_kernel<TIn, D, true><<<grid, kKvWarps * 32, 0, stream>>>(p, err);
+    else gdn_kv_append_kernel<TIn, D, false><<<grid, kKvWarps * 32, 0, stream>>>(p, err);
+}
+template <typename TOut, int D>
+static void launch_read(const KvReadParams& p, bool e4m3, unsigned grid, unsigned* err, cudaStream_t stream) {
+    if (e4m3) gdn_kv_read_kernel<TOut, D, true><<<grid, kKvWarps * 32, 0, stream>>>(p, err);
+    else gdn_kv_read_kernel<TOut, D, false><<<grid, kKvWarps * 32, 0, stream>>>(p, err);
+}
+
+// ---- attention
+// Which kernels a call launches, and its workspace: a function of the sizes that the host knows.
+struct AttnPlan {
+    int dec_grid;
+    size_t bytes, desc, part, ml;  // offsets of the decode kernel's arrays
+};
+static AttnPlan attn_plan(int d) {
+    AttnPlan a = {};
+    a.dec_grid = kAttnSms * (d == 64 ? 2 : 1);
+    a.desc = 0;
+    a.ml = (size_t)a.dec_grid * kDescInts * sizeof(int);
+    a.part = a.ml + (size_t)a.dec_grid * 2 * kDecRows * 2 * sizeof(float);
+    a.bytes = a.part + (size_t)a.dec_grid * 2 * kDecRows * d * sizeof(float);
+    return a;
+}
+
+template <int D, bool E4M3>
+static gdn_status launch_decode_attn(const AttnParams& p, int grid, unsigned* err, cudaStream_t stream) {
+    auto kern = gdn_attn_decode_kernel<D, E4M3>;
+    constexpr size_t smem = DecTraits<D, E4M3>::smem;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+    kern<<<grid, kDecThreads, smem, stream>>>(p, err);
+    e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+// ---- norm
+// Threads of a row and units of 8 channels per thread.  A warp takes rows of up to 1024 channels, more warps longer
+// ones, so that a thread holds at most four units.
+static void norm_shape(int d, int* tpr, int* nv) {
+    const int units = d / 8;
+    *tpr = units <= 128 ? 32 : units <= 512 ? 128 : units <= 1024 ? 256 : 512;
+    const int per = (units + *tpr - 1) / *tpr;
+    *nv = per <= 1 ? 1 : per <= 2 ? 2 : 4;
+}
+
+template <typename T, int OUT>
+static void launch_norm(const NormParams& p, cudaStream_t stream) {
+    int tpr, nv;
+    norm_shape(p.d, &tpr, &nv);
+    const dim3 block(tpr, tpr == 32 ? 4 : 1);
+    const unsigned grid = (unsigned)((p.rows + block.y - 1) / block.y);
+    if (nv == 1) gdn_add_rmsnorm_kernel<T, 1, OUT><<<grid, block, 0, stream>>>(p);
+    else if (nv == 2) gdn_add_rmsnorm_kernel<T, 2, OUT><<<grid, block, 0, stream>>>(p);
+    else gdn_add_rmsnorm_kernel<T, 4, OUT><<<grid, block, 0, stream>>>(p);
+}
+
+template <typename T>
+static void launch_norm_bwd(const NormBwdParams& p, cudaStream_t stream) {
+    int tpr, nv;
+    norm_shape(p.d, &tpr, &nv);
+    if (nv == 1) gdn_add_rmsnorm_bwd_kernel<T, 1><<<p.parts, tpr, 0, stream>>>(p);
+    else if (nv == 2) gdn_add_rmsnorm_bwd_kernel<T, 2><<<p.parts, tpr, 0, stream>>>(p);
+    else gdn_add_rmsnorm_bwd_kernel<T, 4><<<p.parts, tpr, 0, stream>>>(p);
+}
+
+static gdn_status check_norm(long long rows, int d, gdn_dtype dt) {
+    if (rows < 0 || rows > 0x7fffffffLL) return fail(GDN_ERR_INVALID_ARG, "rows must be in [0, 2^31) (got %lld)", rows);
+    if (d < 8 || d > 16384 || d % 8 != 0)
+        return fail(GDN_ERR_UNSUPPORTED, "d must be a multiple of 8 in [8, 16384] (got %d)", d);
+    if (dt != GDN_F32 && dt != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "unknown dtype %d", (int)dt);
+    return GDN_OK;
+}
+
+}  // namespace gdn
+
+using namespace gdn;
+
+extern "C" {
+
+gdn_status gdn_kv_append(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                         void* v_cache, uint8_t* k_scale, uint8_t* v_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* cu_seqlens, int n_tok, int n_seqs, int n_pages,
+                         int max_pages, int page_size, int Hkv, int d, gdn_dtype dt, gdn_dtype cache_dt,
+                         cudaStream_t stream) {
+    clear_error();
+    KvAppendParams p;
+    gdn_status st = check_cache(&p.c, k_cache, v_cache, k_scale, v_scale, block_table, n_tok, n_seqs, n_pages, max_pages,
+                                page_size, Hkv, d, cache_dt);
+    if (st != GDN_OK) return st;
+    if (dt != GDN_F32 && dt != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "k and v are GDN_F32 or GDN_BF16 (got %d)", (int)dt);
+    if (n_tok == 0) return GDN_OK;
+    if ((st = check_ptrs({k, v, seq_lens}, {cu_seqlens})) != GDN_OK) return st;
+    const int esize = dt == GDN_F32 ? 4 : 2;
+    if ((st = check_stride("k_stride", k_stride, (long long)Hkv * d, esize)) != GDN_OK) return st;
+    if ((st = check_stride("v_stride", v_stride, (long long)Hkv * d, esize)) != GDN_OK) return st;
+    if (!cu_seqlens && n_tok % n_seqs != 0)
+        return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens the tokens must divide evenly (%d over %d)", n_tok, n_seqs);
+    unsigned* err = err_word_ptr(&st);
+    if (!err) return st;
+    p.c.seq_lens = seq_lens;
+    p.c.cu = cu_seqlens;
+    p.x[0] = k, p.x[1] = v;
+    p.stride[0] = k_stride, p.stride[1] = v_stride;
+    const unsigned grid = (n_tok + kKvWarps - 1) / kKvWarps;
+    const bool e = cache_dt == GDN_E4M3;
+    ProfScope prof(PK_KV_APPEND, stream);
+    if (dt == GDN_F32) d == 64 ? launch_append<float, 64>(p, e, grid, err, stream) : launch_append<float, 128>(p, e, grid, err, stream);
+    else d == 64 ? launch_append<__nv_bfloat16, 64>(p, e, grid, err, stream) : launch_append<__nv_bfloat16, 128>(p, e, grid, err, stream);
+    prof.done();
+    const cudaError_t ce = cudaGetLastError();
+    if (ce != cudaSuccess) return fail(GDN_ERR_CUDA, "cache append kernel launch: %s", cudaGetErrorString(ce));
+    return GDN_OK;
+}
+
+gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                       const int32_t* block_table, const int32_t* cu_seqlens, void* k, void* v, int n_rows, int n_seqs,
+                       int n_pages, int max_pages, int page_size, int Hkv, int d, gdn_dtype cache_dt, gdn_dtype dt,
+                       cudaStream_t stream) {
+    clear_error();
+    KvReadParams p;
+    gdn_status st = check_cache(&p.c, k_cache, v_cache, k_scale, v_scale, block_table, n_rows, n_seqs, n_pages,
+                                max_pages, page_size, Hkv, d, cache_dt);
+    if (st != GDN_OK) return st;
+    if (dt != GDN_F32 && dt != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "k and v are GDN_F32 or GDN_BF16 (got %d)", (int)dt);
+    if (n_rows == 0) return GDN_OK;
+    if ((st = check_ptrs({cu_seqlens, k, v}, {})) != GDN_OK) return st;
+    unsigned* err = err_word_ptr(&st);
+    if (!err) return st;
+    p.c.cu = cu_seqlens;
+    p.y[0] = k, p.y[1] = v;
+    const unsigned grid = (n_rows + kKvWarps - 1) / kKvWarps;
+    const bool e = cache_dt == GDN_E4M3;
+    ProfScope prof(PK_KV_READ, stream);
+    if (dt == GDN_F32) d == 64 ? launch_read<float, 64>(p, e, grid, err, stream) : launch_read<float, 128>(p, e, grid, err, stream);
+    else d == 64 ? launch_read<__nv_bfloat16, 64>(p, e, grid, err, stream) : launch_read<__nv_bfloat16, 128>(p, e, grid, err, stream);
+    prof.done();
+    const cudaError_t ce = cudaGetLastError();
+    if (ce != cudaSuccess) return fail(GDN_ERR_CUDA, "cache read kernel launch: %s", cudaGetErrorString(ce));
+    return GDN_OK;
+}
+
+size_t gdn_paged_attn_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int d) {
+    if (n_tok < 1 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
+    return attn_plan(d).bytes;
+}
+
+gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                              const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu_seqlens, float scale, int window, void* o,
+                              float* lse, int n_tok, int n_seqs, int n_pages, int max_pages, int page_size, int Hq,
+                              int Hkv, int d, gdn_dtype cache_dt, gdn_dtype o_dt, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream) {
+    clear_error();
+    AttnParams p = {};
+    gdn_status st = check_cache(&p.c, k_cache, v_cache, k_scale, v_scale, block_table, n_tok, n_seqs, n_pages, max_pages,
+                                page_size, Hkv, d, cache_dt);
+    if (st != GDN_OK) return st;
+    if (Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 256)
+        return fail(GDN_ERR_INVALID_ARG, "Hq must be 1 to 256 times Hkv (got %d, %d)", Hq, Hkv);
+    if (o_dt != GDN_F32 && o_dt != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "o is GDN_F32 or GDN_BF16 (got %d)", (int)o_dt);
+    if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite");
+    if (window < 0) return fail(GDN_ERR_INVALID_ARG, "window must be >= 0 (got %d)", window);
+    if ((long long)n_tok * (Hq / Hkv) > 0x7fffff00LL) return fail(GDN_ERR_UNSUPPORTED, "too many query rows");
+    if (n_tok == 0) return GDN_OK;
+    if ((st = check_ptrs({q, seq_lens, o}, {cu_seqlens, lse, workspace})) != GDN_OK) return st;
+    if ((st = check_stride("q_stride", q_stride, (long long)Hq * d, 2)) != GDN_OK) return st;
+    if (!cu_seqlens && n_tok % n_seqs != 0)
+        return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens the tokens must divide evenly (%d over %d)", n_tok, n_seqs);
+    const AttnPlan plan = attn_plan(d);
+    if (!workspace || ws_bytes < plan.bytes)
+        return fail(GDN_ERR_INVALID_ARG, "the attention needs %zu bytes of workspace (got %zu)", plan.bytes, ws_bytes);
+    unsigned* err = err_word_ptr(&st);
+    if (!err) return st;
+    p.c.seq_lens = seq_lens;
+    p.c.cu = cu_seqlens;
+    p.q = static_cast<const __nv_bfloat16*>(q);
+    p.q_stride = q_stride;
+    p.o = o;
+    p.lse = lse;
+    p.scale_log2 = scale * kLog2e;
+    p.window = window;
+    p.G = Hq / Hkv;
+    p.hq = Hq;
+    p.o_f32 = o_dt == GDN_F32;
+    uint8_t* ws = static_cast<uint8_t*>(workspace);
+    p.desc = reinterpret_cast<int*>(ws + plan.desc);
+    p.ml = reinterpret_cast<float*>(ws + plan.ml);
+    p.part = reinterpret_cast<float*>(ws + plan.part);
+    p.rows_lo = 0;
+    p.rows_hi = 0x7fffffff;
+    const bool e = cache_dt == GDN_E4M3;
+    ProfScope prof(PK_ATTN, stream);
+    if (d == 64) st = e ? launch_decode_attn<64, true>(p, plan.dec_grid, err, stream) : launch_decode_attn<64, false>(p, plan.dec_grid, err, stream);
+    else st = e ? launch_decode_attn<128, true>(p, plan.dec_grid, err, stream) : launch_decode_attn<128, false>(p, plan.dec_grid, err, stream);
+    if (st != GDN_OK) return st;
+    JoinParams j = {};
+    j.desc[0] = p.desc, j.part[0] = p.part, j.ml[0] = p.ml, j.grid[0] = plan.dec_grid, j.rows[0] = kDecRows;
+    j.o = o, j.lse = lse, j.G = p.G, j.hq = Hq, j.d = d, j.o_f32 = p.o_f32;
+    const cudaError_t ce = launch_after(gdn_attn_join_kernel, dim3(plan.dec_grid, kDecRows / kJoinRows), dim3(kJoinThreads), stream, j);
+    prof.done();
+    if (ce != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(ce));
+    return GDN_OK;
+}
+
+gdn_status gdn_add_rmsnorm_fwd(const void* x, const void* residual, const float* weight, void* s, void* y,
+                               float* y_scale, float* rstd, long long rows, int d, gdn_dtype dt, gdn_dtype y_dt,
+                               int group, float eps, cudaStream_t stream) {
+    clear_error();
+    gdn_status st = check_norm(rows, d, dt);
+    if (st != GDN_OK) return st;
+    if (y_dt != dt && y_dt != GDN_E4M3)
+        return fail(GDN_ERR_UNSUPPORTED, "y is GDN_E4M3 or has the input's dtype (got %d)", (int)y_dt);
+    if (y_dt == GDN_E4M3) {
+        if (group != 0 && group != kNormGroup)
+            return fail(GDN_ERR_UNSUPPORTED, "group must be 0 (one scale per row) or %d (got %d)", kNormGroup, group);
+        if (group && d % group != 0) return fail(GDN_ERR_UNSUPPORTED, "d must be a multiple of the group (got %d)", d);
+    } else if (group != 0 || y_scale) {
+        return fail(GDN_ERR_INVALID_ARG, "group and y_scale go with an 8-bit output only");
+    }
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(GDN_ERR_INVALID_ARG, "eps must be >= 0");
+    if (rows == 0) return GDN_OK;
+    if ((st = check_ptrs({x, weight, y}, {residual, s, y_scale, rstd})) != GDN_OK) return st;
+    if (y_dt == GDN_E4M3 && !y_scale) return fail(GDN_ERR_INVALID_ARG, "an 8-bit output needs y_scale");
+    const NormParams p{x, residual, weight, s, y, y_scale, rstd, rows, d, eps};
+    ProfScope prof(PK_RMSNORM, stream);
+    if (dt == GDN_F32) {
+        if (y_dt != GDN_E4M3) launch_norm<float, NORM_SAME>(p, stream);
+        else group ? launch_norm<float, NORM_GROUP>(p, stream) : launch_norm<float, NORM_ROW>(p, stream);
+    } else {
+        if (y_dt != GDN_E4M3) launch_norm<__nv_bfloat16, NORM_SAME>(p, stream);
+        else group ? launch_norm<__nv_bfloat16, NORM_GROUP>(p, stream) : launch_norm<__nv_bfloat16, NORM_ROW>(p, stream);
+    }
+    prof.done();
+    const cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm kernel launch: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+size_t gdn_add_rmsnorm_bwd_workspace_bytes(long long rows, int d) {
+    if (rows < 1 || d < 8 || d > 16384 || d % 8 != 0) return 0;
+    return (size_t)norm_bwd_parts(rows) * d * sizeof(float);
+}
+
+gdn_status gdn_add_rmsnorm_bwd(const void* dy, const void* s, const float* weight, const float* rstd, const void* ds,
+                               void* dx, float* dweight, long long rows, int d, gdn_dtype dt, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream) {
+    clear_error();
+    gdn_status st = check_norm(rows, d, dt);
+    if (st != GDN_OK) return st;
+    if ((st = check_ptrs({weight, dweight}, {workspace})) != GDN_OK) return st;
+    if (rows == 0) {  // the gradient of no rows
+        const cudaError_t e = cudaMemsetAsync(dweight, 0, (size_t)d * sizeof(float), stream);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm backward: %s", cudaGetErrorString(e));
+        return GDN_OK;
+    }
+    if ((st = check_ptrs({dy, s, rstd, dx}, {ds})) != GDN_OK) return st;
+    const size_t need = gdn_add_rmsnorm_bwd_workspace_bytes(rows, d);
+    if (!workspace || ws_bytes < need)
+        return fail(GDN_ERR_INVALID_ARG, "the norm's backward pass needs %zu bytes of workspace (got %zu)", need, ws_bytes);
+    const NormBwdParams p{dy, s, weight, rstd, ds, dx, static_cast<float*>(workspace), dweight, rows, d, norm_bwd_parts(rows)};
+    ProfScope prof(PK_RMSNORM_BWD, stream);
+    if (dt == GDN_F32) launch_norm_bwd<float>(p, stream);
+    else launch_norm_bwd<__nv_bfloat16>(p, stream);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm backward kernel launch: %s", cudaGetErrorString(e));
+    e = launch_after(gdn_add_rmsnorm_dw_kernel, dim3((d + 31) / 32), dim3(256), stream, p);
+    prof.done();
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm backward sum kernel launch: %s", cudaGetErrorString(e));
+    return GDN_OK;
+}
+
+}  // extern "C"

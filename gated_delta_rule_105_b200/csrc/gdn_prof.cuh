@@ -14,7 +14,9 @@ namespace gdn {
 
 enum ProfKernel : int {
     PK_SIMT = 0, PK_TC_WY = 1, PK_TC_MAIN = 2, PK_TC2_PREP = 3, PK_TC2_MAIN = 4, PK_DECODE = 5, PK_PRELUDE = 6,
-    PK_OUT_GATE = 7, PK_BWD = 8, PK_COUNT = 9
+    PK_OUT_GATE = 7, PK_BWD = 8,
+    // the attention layer's kernels (9..15 stay unused)
+    PK_KV_APPEND = 16, PK_KV_READ = 17, PK_ATTN = 18, PK_RMSNORM = 19, PK_RMSNORM_BWD = 20, PK_COUNT = 21
 };
 
 struct ProfState {

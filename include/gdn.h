@@ -80,10 +80,11 @@ typedef enum {
     GDN_ERR_UNSUPPORTED = 2,
     GDN_ERR_CUDA = 3,
     GDN_ERR_TIMEOUT = 4,
-    GDN_ERR_DEVICE_ARG = 5 /* reported by gdn_check_error: cu_seqlens out of order or out of range */
+    GDN_ERR_DEVICE_ARG = 5 /* reported by gdn_check_error: cu_seqlens, a sequence length or a page out of range */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype; /* dtype of q, k, v (dt) and of o (o_dt) */
+/* dtype of q, k, v (dt) and of o (o_dt); GDN_E4M3 (8 bits) only where an entry point names it */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* Kernel family used for a call.  AUTO picks the tensor-core (tcgen05) kernel for bf16 inputs when the
  * shape allows it and the SIMT fp32 kernel otherwise.  SIMT forces the fp32-FMA kernel (any dtype); TC
@@ -249,6 +250,90 @@ gdn_status gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, const 
                              int BT, gdn_dtype dt, const int32_t* cu_seqlens, int n_seqs, void* workspace,
                              size_t ws_bytes, cudaStream_t stream);
 
+/* ---------------------------------------------------------------------------------------------------------------
+ * The attention layer beside the token mixer.  Hybrid models put attention layers between gated-delta-rule layers
+ * (Gated DeltaNet-2 article, section "Diseno de bloques y modelo hibrido": a sliding window of 2048; the
+ * walkthrough's model configurations: local attention every other layer).  The pages print no code for them; the
+ * definitions below are the usual ones and complete.
+ *
+ * Paged key/value cache.  k_cache, v_cache [n_pages][Hkv][page_size][d] hold pages of page_size consecutive positions
+ * for every KV head; block_table int32 [n_seqs][max_pages] names the page of positions [i page_size, (i + 1)
+ * page_size) of each sequence (entries behind a sequence's last page are not read and may hold anything).  Pages
+ * may be shared by sequences that only read them.  cache_dt:
+ *   GDN_BF16  bf16 rows; k_scale and v_scale NULL.
+ *   GDN_E4M3  8-bit codes and one scale byte per row, k_scale, v_scale uint8 [n_pages][Hkv][page_size]: a row's values
+ *             are code * 2^(byte - 127), with the smallest exponent in [-117, 119] that keeps every code within 448
+ *             (then every value is exact in bf16; finite values beyond 448 * 2^119 saturate).  A row that holds an
+ *             infinity or a NaN has byte 255 and reads back as NaN throughout.  The codes 0x7f and 0xff (e4m3's
+ *             NaN) are never written and must not be put there by other means.
+ * seq_lens int32 [n_seqs]: positions of each sequence in the cache, the call's new tokens among them.  New tokens are
+ * packed: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 of the n_tok rows (int32 [n_seqs + 1], not
+ * decreasing, within [0, n_tok]; rows behind cu_seqlens[n_seqs] belong to nobody and are neither read nor written), or,
+ * with cu_seqlens NULL, n_tok / n_seqs rows each.  The last new token sits at position seq_lens[n] - 1.
+ * Limits: d in {64, 128}; page_size in {16, 32, 64, 128}; n_seqs <= 65535; Hkv <= 1024; n_pages * Hkv * page_size <
+ * 2^31; max_pages * page_size < 2^31 - 255.  Pointers 16-byte aligned.  Asynchronous on `stream`, no allocation; host
+ * checks first, as for gdn_chunk_fwd.  What only the device can see is reported by gdn_check_error as
+ * GDN_ERR_DEVICE_ARG, without a fault: cu_seqlens out of order (the call's rows are then undefined); a sequence
+ * length below its new tokens or beyond the block table (that sequence is skipped: nothing of it is written); a page
+ * outside the pool (gdn_kv_append and gdn_kv_read skip its rows; gdn_paged_attn_fwd's rows that would have seen it are
+ * undefined). */
+
+/* Writes new tokens' keys and values into their pages.  k, v [n_tok][Hkv][d] in `dt` (fp32 or bf16), token rows
+ * k_stride, v_stride elements apart (>= Hkv d, a multiple of 16 bytes: slices of a fused projection need no copy).
+ * Two tokens must not share a place.  Rounding: nearest, ties to even, once. */
+gdn_status gdn_kv_append(const void* k, const void* v, long long k_stride, long long v_stride, void* k_cache,
+                         void* v_cache, uint8_t* k_scale, uint8_t* v_scale, const int32_t* block_table,
+                         const int32_t* seq_lens, const int32_t* cu_seqlens, int n_tok, int n_seqs, int n_pages,
+                         int max_pages, int page_size, int Hkv, int d, gdn_dtype dt, gdn_dtype cache_dt,
+                         cudaStream_t stream);
+
+/* Reads the cache back as dense rows: k, v [n_rows][Hkv][d] in `dt` (fp32 or bf16, both exact).  Rows cu_seqlens[n] ..
+ * cu_seqlens[n + 1] - 1 are positions 0, 1, ... of sequence n; rows behind cu_seqlens[n_seqs] are left as they were. */
+gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* k_scale, const uint8_t* v_scale,
+                       const int32_t* block_table, const int32_t* cu_seqlens, void* k, void* v, int n_rows, int n_seqs,
+                       int n_pages, int max_pages, int page_size, int Hkv, int d, gdn_dtype cache_dt, gdn_dtype dt,
+                       cudaStream_t stream);
+
+/* Causal attention of the new tokens over the cache (which holds their own keys and values already): one token per
+ * sequence (decoding), chunks of prompts, or both in one call.  For the token at position i, head hq:
+ *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  over j <= i, and j > i - window when window > 0,
+ * with the keys and values of KV head hq / (Hq / Hkv).  lse [n_tok][Hq] fp32 (NULL: not written) is the natural
+ * logarithm of the denominator.  q [n_tok][Hq][d] bf16, token rows q_stride elements apart (>= Hq d, a multiple of 8);
+ * o [n_tok][Hq][d] contiguous, bf16 or fp32.  Keys that a token does not see do not reach it, whatever they hold; a
+ * token that sees a NaN, or an infinity in a value, gets non-finite outputs.  Scores, maxima, sums and outputs
+ * are kept in fp32; the probabilities are rounded to bf16 for the product with V.
+ * Hq / Hkv up to 256.  Workspace: gdn_paged_attn_workspace_bytes() bytes, scratch as for gdn_chunk_fwd (not to be
+ * shared by calls in flight at the same time).  The grid depends on the sizes given here alone, so a captured call can
+ * be replayed after seq_lens, cu_seqlens, block_table and the cache changed.  Equal inputs give equal bits. */
+size_t gdn_paged_attn_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int d);
+gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
+                              const uint8_t* k_scale, const uint8_t* v_scale, const int32_t* block_table,
+                              const int32_t* seq_lens, const int32_t* cu_seqlens, float scale, int window, void* o,
+                              float* lse, int n_tok, int n_seqs, int n_pages, int max_pages, int page_size, int Hq,
+                              int Hkv, int d, gdn_dtype cache_dt, gdn_dtype o_dt, void* workspace, size_t ws_bytes,
+                              cudaStream_t stream);
+
+/* The residual stream's RMS norm, before the projections of an attention or a mixer layer: s = x + residual (residual
+ * NULL: s = x), rstd = 1 / sqrt(mean(s^2) + eps) per row, y = s * rstd * weight.  x, residual, s [rows][d] in `dt`
+ * (fp32 or bf16); weight [d] fp32; s (NULL: not written) may be x or residual itself, no other output may overlap an
+ * input; rstd [rows] fp32 (NULL: not written).  The norm reads the sum before its rounding to `dt`.  y is in `dt`, or
+ * GDN_E4M3 with scales: value = code * y_scale, y_scale = max(largest |y|, 1e-30) / 448 (NaN if one is NaN) over a row
+ * (group 0, y_scale [rows]) or over 128 channels (group 128, y_scale [rows][d / 128], d a multiple of 128).
+ * d a multiple of 8 in [8, 16384].  Asynchronous, no allocation. */
+gdn_status gdn_add_rmsnorm_fwd(const void* x, const void* residual, const float* weight, void* s, void* y,
+                               float* y_scale, float* rstd, long long rows, int d, gdn_dtype dt, gdn_dtype y_dt,
+                               int group, float eps, cudaStream_t stream);
+
+/* Backward pass of gdn_add_rmsnorm_fwd.  dy [rows][d] is the gradient of y (of the values before an 8-bit rounding,
+ * which passes gradients straight through), ds (NULL: none) the one that reaches s by the residual path; s and rstd
+ * are the forward's.  dx [rows][d] in `dt` is the gradient of x and, the same, of residual:
+ *   dx = ds + rstd (w dy - xhat mean(w dy xhat)), xhat = s rstd;   dweight[d] fp32 = sum over rows of dy xhat.
+ * dx may be dy or ds itself.  Workspace: gdn_add_rmsnorm_bwd_workspace_bytes() bytes.  Equal inputs give equal bits. */
+size_t gdn_add_rmsnorm_bwd_workspace_bytes(long long rows, int d);
+gdn_status gdn_add_rmsnorm_bwd(const void* dy, const void* s, const float* weight, const float* rstd, const void* ds,
+                               void* dx, float* dweight, long long rows, int d, gdn_dtype dt, void* workspace,
+                               size_t ws_bytes, cudaStream_t stream);
+
 /* Selects the kernel family for later calls from any thread (process-wide; default AUTO). */
 gdn_status gdn_set_kernel(gdn_kernel kernel);
 
@@ -288,7 +373,8 @@ gdn_status gdn_debug_umma_selftest(const float* A, const float* B, float* D, int
  * gdn_profile_take(kernel, &launches, &total_ms) waits for the recorded events of one kernel -- 0: SIMT
  * kernel, 1: tensor-core WY kernel, 2: tensor-core chunk kernel, 3: GDN-2 / KDA prep kernel, 4: GDN-2 / KDA
  * chunk kernel, 5: decode kernel, 6: prelude kernel, 7: output gate kernel, 8: the backward's two kernels
- * (its forward recompute counts as 0) -- returns how many launches they cover and
+ * (its forward recompute counts as 0), 16: cache append, 17: cache read, 18: paged attention (all launches of a
+ * call as one), 19: residual norm, 20: its backward -- returns how many launches they cover and
  * their summed device time in milliseconds, and forgets them.  Errors: GDN_ERR_INVALID_ARG for an unknown
  * kernel id or NULL outputs, GDN_ERR_CUDA if an event failed. */
 gdn_status gdn_profile_enable(int on);

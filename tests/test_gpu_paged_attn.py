@@ -1,0 +1,302 @@
+"""Attention of new tokens over the paged cache against the fp64 definition (bounds: attn_util)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle.attn as oa
+from attn_util import Cache, attn_excess, attn_reference, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def lib():
+    import gated_delta_rule_105_b200 as g
+    return g
+
+
+def queries(c, hq, seed, size=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (size * torch.randn(c.n_tok, hq, c.d, generator=g)).bfloat16()
+
+
+def call(c, q, dev=None, cu=True, **kw):
+    g = lib()
+    dev = c.cuda() if dev is None else dev
+    o, lse = g.paged_attn_fwd(q if q.is_cuda else q.cuda(), dev["kc"], dev["vc"], dev["table"], dev["lens"],
+                              dev["cu"] if cu else None, dev["ks"], dev["vs"], return_lse=True, **kw)
+    g.check_error()
+    return o, lse
+
+
+def check(c, hq, seed, window=0, o_dtype=torch.bfloat16, scale=None, size=1.0, **kw):
+    q = queries(c, hq, seed, size)
+    scale = c.d ** -0.5 if scale is None else scale
+    o, lse = call(c, q, window=window, o_dtype=o_dtype, scale=scale, **kw)
+    ref = attn_reference(c, f64(q), scale, window)
+    eo, el = attn_excess(o, lse, ref, c, window, o_dtype)
+    assert eo <= 1.0 and el <= 1.0, (eo, el)
+    return o, lse, ref
+
+
+# (positions, new tokens), query heads, KV heads, channels, page, window: single tokens, chunks, mixes, empty and odd
+CASES = [
+    ([1], [1], 1, 1, 64, 16, 0), ([1], [1], 16, 1, 128, 128, 0), ([17], [1], 3, 1, 128, 16, 0), ([128], [1], 4, 2, 64, 32, 0),
+    ([129, 1, 255, 256, 257], [1] * 5, 8, 2, 128, 64, 0), ([1000, 3, 513], [1, 1, 1], 10, 2, 64, 16, 0),
+    ([1000, 3, 513], [1, 1, 1], 10, 2, 128, 16, 100), ([300, 40], [4, 4], 12, 4, 128, 32, 0), ([33, 70], [33, 7], 2, 2, 64, 16, 0),
+    ([200, 64, 5], [200, 1, 5], 4, 2, 128, 64, 0), ([150, 300, 90], [0, 40, 0], 6, 2, 64, 32, 0),
+    ([260, 90], [130, 90], 8, 1, 128, 16, 0), ([260, 90, 31], [130, 90, 2], 8, 4, 64, 128, 50), ([400], [300], 4, 4, 128, 64, 129),
+    ([140, 20], [140, 20], 5, 1, 64, 16, 1), ([520], [260], 2, 1, 128, 128, 0), ([90, 1400], [90, 3], 20, 1, 64, 64, 0)]
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("total,new,hq,hkv,d,page,window", CASES)
+def test_matches_the_definition(kind, total, new, hq, hkv, d, page, window):
+    c = Cache(total, new, hkv, d, page, kind, seed=sum(total) + hq).fill()
+    check(c, hq, 3, window)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new", [1, 70])
+def test_fp32_output_and_other_scales(kind, d, new):
+    c = Cache([200, 90], [new, new], 2, d, 32, kind, seed=new + d).fill(kscale=3.0, vscale=50.0)
+    check(c, 6, 5, 0, torch.float32, scale=0.5, size=2.0)
+    check(c, 6, 5, 0, torch.float32, scale=0.0)
+    check(c, 6, 5, 40, torch.float32, scale=-0.1)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 4, 100])
+def test_growing_scores(kind, new):
+    """Keys whose scores rise along the sequence by far more than fp32's exponent of 2 holds: the running maximum moves
+    in every block, and the sums so far have to be scaled down each time."""
+    L = 700
+    c = Cache([L], [new], 1, 64, 16, kind, seed=1).fill()
+    for pos in range(L):
+        x = c.rng.standard_normal((1, 64)) * 0.1
+        x[0, 0] = 0.5 * pos
+        c.put("k", c.table[0, pos // 16], pos % 16, x)
+    q = queries(c, 2, 1)
+    q[:, :, 0] = 8.0
+    o, lse = call(c, q)
+    ref = attn_reference(c, f64(q), 64 ** -0.5, 0)
+    eo, el = attn_excess(o, lse, ref, c, 0, torch.bfloat16)
+    assert eo <= 1.0 and el <= 1.0
+    q[:, :, 0] = -8.0  # and falling ones
+    o, lse = call(c, q)
+    eo, el = attn_excess(o, lse, attn_reference(c, f64(q), 64 ** -0.5, 0), c, 0, torch.bfloat16)
+    assert eo <= 1.0 and el <= 1.0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,hq,window", [(1, 4, 0), (3, 4, 30), (60, 4, 0), (60, 4, 25), (200, 2, 90)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+def test_what_a_token_does_not_see_does_not_reach_it(kind, new, hq, window, value):
+    """NaN or infinity in the keys and values of one new token: earlier tokens, and later ones whose window has passed
+    it, come out as without it; the tokens that see it are not finite."""
+    L = 230
+    c = Cache([L, 40], [new, 1], 2, 64, 16, kind, seed=new).fill()
+    q = queries(c, hq, 2)
+    clean, clean_lse = call(c, q, window=window)
+    bad = new // 2
+    pos = L - new + bad
+    x = np.zeros((2, 64))
+    x[:, 5] = value
+    pg, r = c.table[0, pos // 16], pos % 16
+    for which in ("v", "k"):
+        c.put(which, pg, r, x)
+        o, lse = call(c, q, window=window)
+        for t in range(new):
+            seen = t >= bad and (not window or t < bad + window)
+            if seen:
+                assert not torch.isfinite(o[t]).all()
+            else:
+                assert torch.equal(o[t], clean[t]) and torch.equal(lse[t], clean_lse[t]), (which, t)
+        assert torch.equal(o[new:], clean[new:])
+
+
+@pytest.mark.parametrize("new", [1, 5, 90])
+@pytest.mark.parametrize("d,hq,hkv,page,window", [(64, 4, 2, 16, 0), (128, 8, 1, 64, 77)])
+def test_8_bit_cache_is_its_read_back(new, d, hq, hkv, page, window):
+    """Dequantised rows are exact in bf16, so attention over the 8-bit cache is that over the read-back rows in a bf16
+    cache; P is rounded with V's power of two in it, which shifts nothing but the exponent."""
+    g = lib()
+    total = [333, 90, 150]
+    c = Cache(total, [min(new, t) for t in total], hkv, d, page, "e4m3", seed=d + new).fill(kscale=4.0, vscale=0.3)
+    q = queries(c, hq, 4)
+    dev = c.cuda()
+    o8, l8 = call(c, q, dev, window=window)
+    cu = torch.tensor(np.concatenate([[0], np.cumsum(total)]), dtype=torch.int32, device="cuda")
+    k, v = g.kv_read(dev["kc"], dev["vc"], dev["table"], cu, sum(total), dev["ks"], dev["vs"])
+    kc = torch.full(dev["kc"].shape, float("nan"), dtype=torch.bfloat16, device="cuda")
+    vc = kc.clone()
+    lens = torch.tensor(total, dtype=torch.int32, device="cuda")
+    g.kv_append(k, v, kc, vc, dev["table"], lens, cu)
+    o16, l16 = call(c, q, {**dev, "kc": kc, "vc": vc, "ks": None, "vs": None}, window=window)
+    # same products and weights, added in other orders: twice the sums' share of the bound
+    ref = attn_reference(c, f64(q), d ** -0.5, window)
+    assert np.all(np.abs(f64(o8) - f64(o16)) <= 2.0 ** -7 * np.abs(ref[0]) + ref[2] * (2.0 ** -7 + 2.0 ** -12))
+    assert np.all(np.abs(f64(l8) - f64(l16)) <= 1e-4)
+
+
+def test_uniform_tokens_without_cu_seqlens_and_strided_queries():
+    c = Cache([100, 64, 31, 250], [3] * 4, 2, 128, 16, "bf16", 21).fill()
+    q = queries(c, 8, 8)
+    a, la = call(c, q)
+    b, lb = call(c, q, cu=False)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    fused = torch.full((12, 8 * 128 + 512), float("nan"), dtype=torch.bfloat16, device="cuda")
+    fused[:, :1024] = q.cuda().view(12, 1024)
+    s, ls = call(c, fused[:, :1024].view(12, 8, 128))
+    assert torch.equal(a, s) and torch.equal(la, ls)
+
+
+def test_rows_behind_the_last_sequence_stay_as_they_were():
+    c = Cache([100, 64], [40, 1], 2, 64, 16, "e4m3", 22).fill()
+    dev = c.cuda()
+    q = torch.randn(50, 4, 64, generator=torch.Generator().manual_seed(1)).bfloat16().cuda()
+    o = torch.full((50, 4, 64), 77.0, dtype=torch.bfloat16, device="cuda")
+    got = lib().paged_attn_fwd(q, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"], dev["ks"], dev["vs"], o=o)
+    lib().check_error()
+    assert got.data_ptr() == o.data_ptr() and (o[41:] == 77).all()
+    ref = attn_reference(c, f64(q[:41]), 0.125, 0)
+    assert np.all(np.abs(f64(o[:41]) - ref[0]) <= 2.0 ** -7 * (ref[2] + np.abs(ref[0])))
+
+
+def test_repeats_to_the_bit_and_two_streams_with_their_own_workspaces():
+    g = lib()
+    cs = [Cache([3000, 500, 1], [1, 1, 1], 2, 128, 64, "bf16", 31).fill(), Cache([900, 300], [200, 1], 2, 128, 64, "bf16", 32).fill()]
+    qs = [queries(c, 8, 9).cuda() for c in cs]
+    devs = [c.cuda() for c in cs]
+    want = [call(c, q, dev) for c, q, dev in zip(cs, qs, devs)]
+    ws = [torch.empty(g.paged_attn_workspace_bytes(c.n_tok, len(c.total), 8, 2, 128), dtype=torch.uint8, device="cuda") for c in cs]
+    streams = [torch.cuda.Stream() for _ in cs]
+    torch.cuda.synchronize()
+    got = [[] for _ in cs]
+    for _ in range(10):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                d = devs[i]
+                got[i].append(g.paged_attn_fwd(qs[i], d["kc"], d["vc"], d["table"], d["lens"], d["cu"], return_lse=True, workspace=ws[i]))
+    torch.cuda.synchronize()
+    for w, all_ in zip(want, got):
+        for o, lse in all_:
+            assert torch.equal(o, w[0]) and torch.equal(lse, w[1])
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_captured_step_replays_with_new_lengths(kind):
+    """A decode step -- append, attend -- captured once and replayed as the sequences grow, pages being added."""
+    g = lib()
+    n, hkv, hq, d, page = 3, 2, 8, 64, 16
+    c = Cache([60, 5, 130], [1] * n, hkv, d, page, kind, 41, spare=8, extra_cols=4).fill(upto_new=False)
+    dev = c.cuda()
+    free = [p for p in range(c.n_pages) if p not in set(c.table[c.table >= 0].tolist())]
+    k, v, q = (torch.zeros(n, h, d, dtype=torch.bfloat16, device="cuda") for h in (hkv, hkv, hq))
+    ws = torch.empty(g.paged_attn_workspace_bytes(n, n, hq, hkv, d), dtype=torch.uint8, device="cuda")
+    o = torch.empty(n, hq, d, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        g.kv_append(k, v, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"], dev["ks"], dev["vs"])
+        return g.paged_attn_fwd(q, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"], dev["ks"], dev["vs"],
+                                o=o, return_lse=True, workspace=ws)[1]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lse = step()
+    gen = torch.Generator().manual_seed(5)
+    for it in range(20):
+        new = [torch.randn(n, h, d, generator=gen).bfloat16() for h in (hkv, hkv, hq)]
+        for t, x in zip((k, v, q), new):
+            t.copy_(x)
+        if it:
+            for i in range(n):
+                c.total[i] += 1
+                if (c.total[i] - 1) % page == 0:
+                    c.table[i, (c.total[i] - 1) // page] = free.pop()
+            dev["table"].copy_(torch.from_numpy(c.table))
+            dev["lens"].copy_(torch.tensor(c.total, dtype=torch.int32))
+        for i in range(n):
+            pos = c.total[i] - 1
+            for which, x in zip(("k", "v"), new):
+                c.put(which, c.table[i, pos // page], pos % page, f64(x[i]))
+        graph.replay()
+        g.check_error()
+        eo, el = attn_excess(o, lse, attn_reference(c, f64(new[2]), d ** -0.5, 0), c, 0, torch.bfloat16)
+        assert eo <= 1.0 and el <= 1.0, it
+
+
+def test_many_sequences_and_a_long_one():
+    rng = np.random.default_rng(3)
+    total = [int(x) for x in rng.integers(1, 40, 400)] + [6000]
+    new = [int(min(t, x)) for t, x in zip(total, rng.integers(0, 3, 401))]
+    c = Cache(total, new, 1, 64, 32, "bf16", 51).fill()
+    check(c, 4, 1)
+
+
+@pytest.mark.parametrize("what", ["page", "len_long", "len_short", "cu_order"])
+@pytest.mark.parametrize("new", [2, 60])
+def test_bad_device_arguments_are_reported(what, new):
+    g = lib()
+    c = Cache([100, 100, 100], [new] * 3, 2, 64, 16, "bf16", 61).fill()
+    q = queries(c, 4, 1).cuda()
+    good, _ = call(c, q)
+    dev = c.cuda()
+    if what == "page":
+        dev["table"][1, 2] = 1 << 30
+    elif what == "len_long":
+        dev["lens"][1] = 1 << 30
+    elif what == "len_short":
+        dev["lens"][1] = new - 1
+    else:
+        dev["cu"][2] = 0
+    o = torch.full_like(good, 5.0)
+    g.paged_attn_fwd(q, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"], o=o)
+    with pytest.raises(g.GdnError) as e:
+        g.check_error()
+    assert e.value.status == 5
+    g.check_error()
+    if what != "cu_order":  # a later sequence then claims the same rows
+        assert torch.equal(o[:new], good[:new]) and torch.equal(o[2 * new:], good[2 * new:])
+        if what != "page":
+            assert (o[new:2 * new] == 5).all()
+
+
+def test_an_attention_layer_beside_a_mixer_layer():
+    """One decode step of a hybrid block as a server runs it: residual norm with 8-bit output, projections, cache write,
+    attention over it, the next residual norm, then the mixer's own decode step; against the same in fp64."""
+    g = lib()
+    n, hq, hkv, d, dm = 4, 8, 2, 128, 512
+    c = Cache([300, 17, 64, 129], [1] * n, hkv, d, 64, "e4m3", 71).fill(upto_new=False)
+    gen = torch.Generator().manual_seed(6)
+    x, r = torch.randn(n, dm, generator=gen).bfloat16(), torch.randn(n, dm, generator=gen).bfloat16()
+    w = 1 + 0.1 * torch.randn(dm, generator=gen)
+    W = torch.randn(dm, (hq + 2 * hkv) * d, generator=gen) / dm ** 0.5
+    dev = c.cuda()
+    norm = g.add_rmsnorm_fwd(x.cuda(), w.cuda(), r.cuda(), out_dtype=torch.float8_e4m3fn, group=128)
+    y = (norm["y"].float().view(n, -1, 128) * norm["scale"][..., None]).view(n, dm)
+    qkv = (y @ W.cuda()).bfloat16()
+    q, k, v = (qkv[:, a:b].view(n, -1, d) for a, b in ((0, hq * d), (hq * d, (hq + hkv) * d), ((hq + hkv) * d, (hq + 2 * hkv) * d)))
+    g.kv_append(k, v, dev["kc"], dev["vc"], dev["table"], dev["lens"], None, dev["ks"], dev["vs"])
+    o, lse = g.paged_attn_fwd(q, dev["kc"], dev["vc"], dev["table"], dev["lens"], None, dev["ks"], dev["vs"], window=128,
+                              return_lse=True)
+    g.check_error()
+    for i in range(n):
+        pos = c.total[i] - 1
+        for which, t in (("k", k), ("v", v)):
+            c.put(which, c.table[i, pos // 64], pos % 64, f64(t[i]))
+    eo, el = attn_excess(o, lse, attn_reference(c, f64(q), d ** -0.5, 128), c, 128, torch.bfloat16)
+    assert eo <= 1.0 and el <= 1.0
+    h = 4
+    state = torch.zeros(n, h, 128, 256, device="cuda")
+    qq, kk = (o.reshape(n, 8, 128)[:, a:a + h].contiguous() for a in (0, 4))
+    vv = torch.cat([qq, kk], -1).contiguous()
+    gate, beta = -torch.ones(n, h, device="cuda"), torch.full((n, h), 0.5, device="cuda")
+    out = g.decode_fwd(qq, kk, vv, gate, beta, state)
+    # from a zero state: o = scale beta (k . q) v
+    want = 128 ** -0.5 * 0.5 * (qq.double() * kk.double()).sum(-1, keepdim=True) * vv.double()
+    assert torch.allclose(out.double(), want, rtol=2.0 ** -6, atol=1e-6)
+    tail = g.add_rmsnorm_fwd(out.reshape(n, -1)[:, :dm].contiguous(), w.cuda(), norm["s"])
+    assert torch.isfinite(tail["y"].float()).all() and tail["s"].shape == (n, dm)

@@ -1,0 +1,137 @@
+"""The residual RMS norm with its 8-bit outputs, and its backward pass, against the fp64 definition.
+
+Bounds.  u is half a step (fp32 2^-24, bf16 2^-8).  A sum of d squares goes through at most 32 additions in a thread,
+5 in a warp and 15 across warps, plus the product and the division: its relative error is below 55 u, the square root
+halves it, and 2 more roundings follow: rstd within 30 u.  y has two more products and the sum x + r (one rounding of
+s, relative to |s|): 33 u |y|, and the output's own rounding.  An 8-bit value is within half a step of e4m3 (2^-4
+relative, 2^-10 scale below its normal range) of y, its scale within 34 u.
+Backward: the mean of n products is off by 60 u mean |gw xhat|; dx = ds + rstd (gw - xhat mean) adds four roundings of
+its terms.  dw sums rows / parts products in a thread, then parts in the second kernel: (rows + 20) u of the sum of
+magnitudes bounds both.
+"""
+import numpy as np
+import pytest
+import torch
+
+import oracle.attn as oa
+from attn_util import U, f64
+
+pytestmark = pytest.mark.gpu
+EPS = 1e-5
+u = 2.0 ** -24
+
+
+def lib():
+    import gated_delta_rule_105_b200 as g
+    return g
+
+
+def draw(rows, d, dt, seed):
+    g = torch.Generator().manual_seed(seed)
+    return [torch.randn(rows, d, generator=g).to(dt), (3 * torch.randn(rows, d, generator=g)).to(dt),
+            1 + 0.3 * torch.randn(d, generator=g)]
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("out,group", [("same", 0), ("e4m3", 0), ("e4m3", 128)])
+@pytest.mark.parametrize("rows,d", [(1, 8), (1, 128), (5, 256), (3, 1024), (2, 1032), (7, 1920), (2, 4096), (3, 5000),
+                                    (2, 8192), (1, 16384), (700, 128)])
+@pytest.mark.parametrize("residual", [True, False])
+def test_forward(dt, out, group, rows, d, residual):
+    if group and d % group:
+        pytest.skip("128-channel scales need d to be a multiple of 128")
+    x, r, w = draw(rows, d, dt, rows * d)
+    r = r if residual else None
+    got = lib().add_rmsnorm_fwd(x.cuda(), w.cuda(), None if r is None else r.cuda(), EPS,
+                                torch.float8_e4m3fn if out == "e4m3" else dt, group)
+    s, rstd, y = oa.add_rmsnorm(f64(x), None if r is None else f64(r), f64(w), EPS)
+    assert np.all(np.abs(f64(got["s"]) - s) <= U[dt] * np.abs(s) * (1 if residual else 0))
+    assert np.all(np.abs(f64(got["rstd"]) - rstd) <= 30 * u * rstd)
+    if out == "same":
+        assert got["scale"] is None
+        assert np.all(np.abs(f64(got["y"]) - y) <= 33 * u * np.abs(y) + U[dt] * np.abs(y) * (1 + 33 * u))
+        return
+    parts = np.abs(y).reshape(rows, -1, group or d)
+    scale = parts.max(-1) / 448
+    gs = f64(got["scale"]).reshape(scale.shape)
+    assert np.all(np.abs(gs - scale) <= 36 * u * scale)
+    val = oa.e4m3_value(got["y"].cpu().view(torch.uint8).numpy()).reshape(parts.shape) * gs[..., None]
+    ys = y.reshape(parts.shape)
+    bound = np.maximum(2.0 ** -4 * np.abs(ys), 2.0 ** -10 * gs[..., None]) + 72 * u * np.abs(ys)
+    assert np.all(np.abs(val - ys) <= bound)
+
+
+def test_stream_updated_in_place_and_zero_and_nan_rows():
+    g = lib()
+    x, r, w = draw(4, 512, torch.bfloat16, 3)
+    x[1], r[1] = 0, 0
+    x[2, 7] = float("nan")
+    rd = r.cuda()
+    got = g.add_rmsnorm_fwd(x.cuda(), w.cuda(), rd, EPS, torch.float8_e4m3fn, 0, s=rd)
+    assert got["s"].data_ptr() == rd.data_ptr()
+    want = g.add_rmsnorm_fwd(x.cuda(), w.cuda(), r.cuda(), EPS, torch.float8_e4m3fn, 0)
+    for k in ("s", "rstd", "scale"):
+        assert torch.equal(torch.nan_to_num(got[k].float(), 7.0), torch.nan_to_num(want[k].float(), 7.0))
+    assert torch.equal(got["y"].view(torch.uint8), want["y"].view(torch.uint8))
+    y = got["y"].float()
+    assert (y[1] == 0).all() and torch.isfinite(got["scale"][1])
+    assert torch.isnan(y[2]).all() and torch.isnan(got["scale"][2])
+    assert torch.isfinite(y[[0, 3]]).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("rows,d", [(1, 8), (2, 128), (5, 1000), (300, 256), (7, 1032), (601, 2048), (3, 4096), (2, 16384)])
+@pytest.mark.parametrize("with_ds", [True, False])
+def test_backward(dt, rows, d, with_ds):
+    g = lib()
+    s, dy, w = draw(rows, d, dt, rows + d)
+    ds = draw(rows, d, dt, 7 * rows + d)[0] if with_ds else None
+    rstd = (1 / torch.sqrt(s.double().square().mean(-1) + EPS)).float()
+    got = g.add_rmsnorm_bwd(dy.cuda(), s.cuda(), w.cuda(), rstd.cuda(), None if ds is None else ds.cuda())
+    S, DY, W, R = f64(s), f64(dy), f64(w), f64(rstd)[:, None]
+    dx, dw = oa.add_rmsnorm_grads(DY, S, W, R[:, 0], None if ds is None else f64(ds))
+    xhat, gw = S * R, DY * W
+    m = np.mean(np.abs(gw * xhat), -1, keepdims=True)
+    terms = np.abs(R * gw) + np.abs(R * xhat) * m + (0 if ds is None else np.abs(f64(ds)))
+    assert np.all(np.abs(f64(got["dx"]) - dx) <= 6 * u * terms + 60 * u * np.abs(R * xhat) * m + U[dt] * np.abs(dx) * (1 + 2.0 ** -7))
+    assert np.all(np.abs(f64(got["dweight"]) - dw) <= (rows + 20) * u * np.sum(np.abs(DY * xhat), 0))
+
+
+def test_backward_in_place_repeats_to_the_bit_and_of_no_rows():
+    g = lib()
+    s, dy, w = draw(400, 640, torch.bfloat16, 1)
+    ds = draw(400, 640, torch.bfloat16, 2)[0]
+    rstd = torch.rsqrt(s.float().square().mean(-1) + EPS)
+    dev = [t.cuda() for t in (dy, s, w, rstd)]
+    a = g.add_rmsnorm_bwd(*dev, ds.cuda())
+    for target in ("dy", "ds"):
+        d2, s2 = dy.cuda(), ds.cuda()
+        b = g.add_rmsnorm_bwd(d2, *dev[1:], s2, dx=d2 if target == "dy" else s2)
+        assert torch.equal(a["dx"], b["dx"]) and torch.equal(a["dweight"], b["dweight"])
+    none = g.add_rmsnorm_bwd(dev[0][:0], dev[1][:0], dev[2], dev[3][:0])
+    assert none["dx"].shape == (0, 640) and (none["dweight"] == 0).all()
+
+
+def test_gradients_agree_with_differences():
+    """Through the forward kernel itself, in fp32: directional differences of <dy, y> + <ds, s>."""
+    g = lib()
+    x, r, w = draw(6, 384, torch.float32, 5)
+    dy, ds, dirs = draw(6, 384, torch.float32, 6)[0], draw(6, 384, torch.float32, 7)[0], draw(6, 384, torch.float32, 8)
+    dw_dir = draw(1, 384, torch.float32, 9)[0][0]
+
+    def loss(x, r, w):
+        o = g.add_rmsnorm_fwd(x.cuda(), w.cuda(), r.cuda(), EPS)
+        return float((o["y"].double().cpu() * dy.double()).sum() + (o["s"].double().cpu() * ds.double()).sum()), o
+
+    _, o = loss(x, r, w)
+    got = g.add_rmsnorm_bwd(dy.cuda(), o["s"], w.cuda(), o["rstd"], ds.cuda())
+    # a step of 2^-6: the difference's own error is its third derivative (relative ~2^-12), and the losses' fp32
+    # roundings, 2304 terms of ~2^-22 in quadrature over 2^-5, are below 1e-3
+    h = 2.0 ** -6
+    for dx, dr, dw in ((dirs[0], 0, 0), (0, dirs[0], 0), (0, 0, dw_dir)):
+        num = (loss(x + h * dx, r + h * dr, w + h * dw)[0] - loss(x - h * dx, r - h * dr, w - h * dw)[0]) / (2 * h)
+        want = float((got["dx"].double().cpu() * (torch.as_tensor(dx) + torch.as_tensor(dr)).double()).sum()
+                     + (got["dweight"].double().cpu() * torch.as_tensor(dw).double()).sum())
+        size = float((got["dx"].double().cpu().abs() * (torch.as_tensor(dx).abs() + torch.as_tensor(dr).abs()).double()).sum()
+                     + (got["dweight"].double().cpu().abs() * torch.as_tensor(dw).abs().double()).sum())
+        assert abs(num - want) <= 2e-3 + 2.0 ** -11 * size
