@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int cta = blockIdx.x, N = p.c.n_seq;
 
+    cudaTriggerProgrammaticLaunchCompletion();  // the next kernel may be brought up while this one runs
     // this CTA's stretch [w0, w1) of all units, and the sequence it starts in
     long long W = 0;
     for (int base = 0; base < N; base += kDecThreads) {
@@ -511,8 +512,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
         }
         if (!whole && x0 == 0 && tid == 0) {  // the item starts here and ends in a later CTA
             const long long end = w + sp.units;
-            int c1 = cta + 1;
-            while (c1 < grid && W * c1 / grid < end) ++c1;
+            const int c1 = (int)((end * grid + W - 1) / W);  // first CTA whose stretch begins at `end` or behind
             desc[0] = n;
             desc[1] = h;
             desc[2] = rg * R;

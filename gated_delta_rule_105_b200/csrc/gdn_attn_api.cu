@@ -5,26 +5,29 @@
 
 #include "gdn.h"
 #include "gdn_attn.cuh"
+#include "gdn_attn_tc.cuh"
 #include "gdn_host.h"
 #include "gdn_norm.cuh"
 #include "gdn_prof.cuh"
 
 namespace gdn {
 
-// Launches `kern` so that it may start while the launch before it on the stream still drains (programmatic stream
-// serialisation); the kernel waits for that launch's memory with cudaGridDependencySynchronize().
-template <typename P>
-static cudaError_t launch_after(void (*kern)(P), dim3 grid, dim3 block, cudaStream_t stream, const P& params) {
+// Launches `kern`; with `early` it may start while the launch before it on the stream still runs (programmatic stream
+// serialisation): the kernel waits for that launch's memory with cudaGridDependencySynchronize().
+template <typename... P, typename... A>
+static cudaError_t launch_after(void (*kern)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream, bool early,
+                                const A&... args) {
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = grid;
     cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, params);
+    cfg.numAttrs = early ? 1 : 0;
+    return cudaLaunchKernelEx(&cfg, kern, P(args)...);
 }
 
 static gdn_status check_ptrs(std::initializer_list<const void*> required, std::initializer_list<const void*> optional) {
@@ -97,30 +100,88 @@ static void launch_read(const KvReadParams& p, bool e4m3, unsigned grid, unsigne
 }
 
 // ---- attention
-// Which kernels a call launches, and its workspace: a function of the sizes that the host knows.
-struct AttnPlan {
-    int dec_grid;
-    size_t bytes, desc, part, ml;  // offsets of the decode kernel's arrays
+// Which kernels a call launches, and its workspace: a function of the sizes that the host knows.  Sequences of up to
+// kDecMaxRows query rows per KV head belong to the decode kernel, longer ones to the chunk kernel.  Where every
+// sequence has as many tokens (no cu_seqlens) or there is but one, one kernel takes the call; a batch with no more
+// tokens than sequences is decoding, and the decode kernel takes all of it; else both run.
+constexpr int kDecMaxRows = 16;
+struct AttnArrays {
+    int grid;  // 0: this kernel is not launched
+    size_t desc, ml, part;
 };
-static AttnPlan attn_plan(int d) {
+struct AttnPlan {
+    AttnArrays dec, tc;
+    int limit;  // the decode kernel's largest row count
+    size_t bytes;
+};
+static AttnPlan attn_plan(int n_tok, int n_seqs, bool packed, int G, int d) {
     AttnPlan a = {};
-    a.dec_grid = kAttnSms * (d == 64 ? 2 : 1);
-    a.desc = 0;
-    a.ml = (size_t)a.dec_grid * kDescInts * sizeof(int);
-    a.part = a.ml + (size_t)a.dec_grid * 2 * kDecRows * 2 * sizeof(float);
-    a.bytes = a.part + (size_t)a.dec_grid * 2 * kDecRows * d * sizeof(float);
+    a.limit = 0x7fffffff;
+    if (n_tok <= n_seqs) {
+        a.dec.grid = 1;
+    } else if (n_seqs == 1 || !packed) {
+        if ((long long)(n_tok / n_seqs) * G <= kDecMaxRows) a.dec.grid = 1;
+        else a.tc.grid = 1, a.limit = 0;
+    } else {
+        a.dec.grid = a.tc.grid = 1;
+        a.limit = kDecMaxRows;
+    }
+    auto place = [&](AttnArrays& r, int grid, int rows) {
+        if (!r.grid) return;
+        r.grid = grid;
+        r.desc = a.bytes;
+        r.ml = r.desc + (size_t)grid * kDescInts * sizeof(int);
+        r.part = r.ml + (size_t)grid * 2 * rows * 2 * sizeof(float);
+        a.bytes = r.part + (size_t)grid * 2 * rows * d * sizeof(float);
+    };
+    place(a.dec, kAttnSms * (d == 64 ? 2 : 1), kDecRows);
+    place(a.tc, kAttnSms, kTcRows);
     return a;
 }
 
+static void use_arrays(AttnParams& p, const AttnArrays& r, uint8_t* ws) {
+    p.desc = reinterpret_cast<int*>(ws + r.desc);
+    p.ml = reinterpret_cast<float*>(ws + r.ml);
+    p.part = reinterpret_cast<float*>(ws + r.part);
+}
+
 template <int D, bool E4M3>
-static gdn_status launch_decode_attn(const AttnParams& p, int grid, unsigned* err, cudaStream_t stream) {
-    auto kern = gdn_attn_decode_kernel<D, E4M3>;
-    constexpr size_t smem = DecTraits<D, E4M3>::smem;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-    kern<<<grid, kDecThreads, smem, stream>>>(p, err);
-    e = cudaGetLastError();
-    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention kernel launch: %s", cudaGetErrorString(e));
+static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, JoinParams& j, unsigned* err, cudaStream_t stream) {
+    cudaError_t e;
+    if (plan.dec.grid) {
+        use_arrays(p, plan.dec, ws);
+        p.rows_lo = 0;
+        p.rows_hi = plan.limit;
+        auto kern = gdn_attn_decode_kernel<D, E4M3>;
+        constexpr size_t smem = DecTraits<D, E4M3>::smem;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        kern<<<plan.dec.grid, kDecThreads, smem, stream>>>(p, err);
+        e = cudaGetLastError();
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention decode kernel launch: %s", cudaGetErrorString(e));
+        j.desc[0] = p.desc, j.part[0] = p.part, j.ml[0] = p.ml, j.grid[0] = plan.dec.grid, j.rows[0] = kDecRows;
+    }
+    if (plan.tc.grid) {
+        use_arrays(p, plan.tc, ws);
+        p.rows_lo = plan.dec.grid ? plan.limit : 0;
+        p.rows_hi = 0x7fffffff;
+        CUtensorMap mk = {}, mv = {};
+        if (!E4M3) {
+            const long long rows = ((long long)p.c.n_pages * p.c.hkv) << p.c.page_log2;
+            if (!make_cache_map(&mk, p.c.k_cache, D, rows, 1 << p.c.page_log2) || !make_cache_map(&mv, p.c.v_cache, D, rows, 1 << p.c.page_log2))
+                return fail(GDN_ERR_CUDA, "cuTensorMapEncodeTiled failed");
+        }
+        auto kern = gdn_attn_chunk_kernel<D, E4M3>;
+        using L = AttnTc<D, E4M3>;
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
+        j.desc[1] = p.desc, j.part[1] = p.part, j.ml[1] = p.ml, j.grid[1] = plan.tc.grid, j.rows[1] = kTcRows;
+    }
+    const unsigned y = (plan.tc.grid ? kTcRows : kDecRows) / kJoinRows;
+    e = launch_after(gdn_attn_join_kernel, dim3(plan.dec.grid + plan.tc.grid, y), dim3(kJoinThreads), 0, stream, true, j);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;
 }
 
@@ -232,7 +293,8 @@ gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* 
 
 size_t gdn_paged_attn_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int d) {
     if (n_tok < 1 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-    return attn_plan(d).bytes;
+    // a call with and one without cu_seqlens may differ: enough for either
+    return std::max(attn_plan(n_tok, n_seqs, true, Hq / Hkv, d).bytes, attn_plan(n_tok, n_seqs, false, Hq / Hkv, d).bytes);
 }
 
 gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -257,7 +319,7 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     if ((st = check_stride("q_stride", q_stride, (long long)Hq * d, 2)) != GDN_OK) return st;
     if (!cu_seqlens && n_tok % n_seqs != 0)
         return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens the tokens must divide evenly (%d over %d)", n_tok, n_seqs);
-    const AttnPlan plan = attn_plan(d);
+    const AttnPlan plan = attn_plan(n_tok, n_seqs, cu_seqlens != nullptr, Hq / Hkv, d);
     if (!workspace || ws_bytes < plan.bytes)
         return fail(GDN_ERR_INVALID_ARG, "the attention needs %zu bytes of workspace (got %zu)", plan.bytes, ws_bytes);
     unsigned* err = err_word_ptr(&st);
@@ -274,23 +336,13 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     p.hq = Hq;
     p.o_f32 = o_dt == GDN_F32;
     uint8_t* ws = static_cast<uint8_t*>(workspace);
-    p.desc = reinterpret_cast<int*>(ws + plan.desc);
-    p.ml = reinterpret_cast<float*>(ws + plan.ml);
-    p.part = reinterpret_cast<float*>(ws + plan.part);
-    p.rows_lo = 0;
-    p.rows_hi = 0x7fffffff;
-    const bool e = cache_dt == GDN_E4M3;
-    ProfScope prof(PK_ATTN, stream);
-    if (d == 64) st = e ? launch_decode_attn<64, true>(p, plan.dec_grid, err, stream) : launch_decode_attn<64, false>(p, plan.dec_grid, err, stream);
-    else st = e ? launch_decode_attn<128, true>(p, plan.dec_grid, err, stream) : launch_decode_attn<128, false>(p, plan.dec_grid, err, stream);
-    if (st != GDN_OK) return st;
     JoinParams j = {};
-    j.desc[0] = p.desc, j.part[0] = p.part, j.ml[0] = p.ml, j.grid[0] = plan.dec_grid, j.rows[0] = kDecRows;
     j.o = o, j.lse = lse, j.G = p.G, j.hq = Hq, j.d = d, j.o_f32 = p.o_f32;
-    const cudaError_t ce = launch_after(gdn_attn_join_kernel, dim3(plan.dec_grid, kDecRows / kJoinRows), dim3(kJoinThreads), stream, j);
+    ProfScope prof(PK_ATTN, stream);
+    if (cache_dt == GDN_E4M3) st = d == 64 ? launch_attn<64, true>(p, plan, ws, j, err, stream) : launch_attn<128, true>(p, plan, ws, j, err, stream);
+    else st = d == 64 ? launch_attn<64, false>(p, plan, ws, j, err, stream) : launch_attn<128, false>(p, plan, ws, j, err, stream);
     prof.done();
-    if (ce != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(ce));
-    return GDN_OK;
+    return st;
 }
 
 gdn_status gdn_add_rmsnorm_fwd(const void* x, const void* residual, const float* weight, void* s, void* y,
@@ -354,7 +406,7 @@ gdn_status gdn_add_rmsnorm_bwd(const void* dy, const void* s, const float* weigh
     else launch_norm_bwd<__nv_bfloat16>(p, stream);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm backward kernel launch: %s", cudaGetErrorString(e));
-    e = launch_after(gdn_add_rmsnorm_dw_kernel, dim3((d + 31) / 32), dim3(256), stream, p);
+    e = launch_after(gdn_add_rmsnorm_dw_kernel, dim3((d + 31) / 32), dim3(256), 0, stream, true, p);
     prof.done();
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "norm backward sum kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;

@@ -1,0 +1,729 @@
+// Paged attention for many query rows (chunks of prompts): tcgen05 kernel.  See gdn_attn.cuh for the operator, the items
+// and how their units are shared out; here an item is 256 query rows of one (sequence, KV head) and a unit is a tile of
+// 128 keys.
+//
+// One CTA per SM.  The 256 rows are two tiles of 128 (the height of one MMA), each with its own softmax warpgroup, so
+// that one tile's softmax runs while the tensor core works for the other:
+//   warp 0        loads K and V tiles: one tensor-map box per (page, 64 channels), a ring of stages each
+//   warp 1        issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor memory)
+//   warps 2, 3    bf16 cache: look for non-finite V rows in tiles that are not wholly visible (see below)
+//   warps 4 - 11  softmax: thread = row, the 128 scores of a tile in registers, P back into the columns of S as bf16
+//   warps 12 - 15 8-bit cache: codes of a tile (bulk copies, one per page) to exact bf16 in the swizzled layout
+// Tensor memory: S/P of both tiles (2 x 128 columns) and O of both (2 x d).  The running maximum is lazy: O is scaled
+// down only when a row's maximum has grown by more than 2^8, which after the first tiles is rare; then the warp reads
+// and writes its part of O itself (the commit that announced S came after the previous P V, so O is at rest).
+//
+// Masked keys.  A score that a row must not see is set to -inf before the maximum, so K may hold anything there.  For V a
+// weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, V rows with a NaN or an infinity
+// are zeroed in shared memory and marked, and rows that do see a marked key take a NaN weight for it.
+#pragma once
+
+#include "gdn_attn.cuh"
+
+namespace gdn {
+
+constexpr int kTcRows = 256, kTcTile = 128;
+
+template <int D, bool E4M3> struct AttnTc {
+    static constexpr int THREADS = E4M3 ? 512 : 384;
+    static constexpr int NK = 2, NV = E4M3 ? 2 : 3, NR = E4M3 ? 2 : 0;  // K, V and raw stages
+    static constexpr int HALF = kTcTile * 128;                          // 64 channels of 128 rows, bf16
+    static constexpr int TILE = HALF * (D / 64);
+    static constexpr int RAW = kTcTile * D;
+    static constexpr int OFF_Q = 0, OFF_K = 2 * TILE, OFF_V = OFF_K + NK * TILE, OFF_RAW = OFF_V + NV * TILE;
+    static constexpr int OFF_SC = OFF_RAW + NR * RAW;       // raw scale bytes
+    static constexpr int OFF_CTL = OFF_SC + NR * kTcTile;   // barriers and the like
+    static constexpr int CTL = 1024;
+    static constexpr int BYTES = OFF_CTL + CTL + 1024;      // + alignment to 1024
+    static_assert(BYTES <= 232448, "shared memory of a block");
+};
+
+struct AttnTcCtl {
+    uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_ready[3], v_empty[3], r_full[2], r_empty[2];
+    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint32_t tmem;
+    volatile int abort_flag;
+    uint32_t bad[3][4];  // marked keys of each V stage's tile
+    // where this CTA's stretch starts
+    long long W, w0, w1;
+    int n, h, rt, x;
+};
+static_assert(sizeof(AttnTcCtl) <= 1024, "control block");
+// Used while the work is shared out, in Q's place.
+struct TcScratch {
+    long long scan[32];
+    long long pre[257];
+};
+
+__device__ __forceinline__ void tma_load_2d(void* dst, const CUtensorMap* map, uint64_t* bar, int c0, int c1) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];" ::"r"(
+            sm100::smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(sm100::smem_u32(bar)), "r"(c0), "r"(c1)
+        : "memory");
+}
+// 32 lanes x 16 consecutive 32-bit columns.
+__device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(ta)
+        : "memory");
+}
+// gdn_sm100.cuh's bounded wait without its out-of-line part: a kernel that moves registers between its warpgroups
+// (setmaxnreg) cannot call functions.
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    const long long t0 = clock64();
+    while (true) {
+        if (*abort_flag) return false;
+        if (sm100::mbar_try_wait(bar, parity)) return true;
+        if (clock64() - t0 > sm100::kWaitLimitCycles) {
+            *abort_flag = 1;
+            atomicOr(err, kErrTimeout);
+            return false;
+        }
+    }
+}
+__device__ __forceinline__ bool tc_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+    return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, err));
+}
+template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+
+// Key tiles [t0, t1) that rows [r0, r1) of a sequence see (r0 < r1 <= rows).
+__device__ __forceinline__ void tile_range(const AttnParams& p, const SeqSpan& s, int r0, int r1, int& t0, int& t1) {
+    const int base = s.len - s.T;
+    t1 = (base + (r1 - 1) / p.G) / kTcTile + 1;
+    t0 = p.window > 0 ? max(0, base + r0 / p.G - p.window + 1) / kTcTile : 0;
+}
+__device__ __forceinline__ int tc_units(const AttnParams& p, const SeqSpan& s, int rt) {
+    int t0, t1;
+    tile_range(p, s, rt * kTcRows, min(s.T * p.G, (rt + 1) * kTcRows), t0, t1);
+    return t1 - t0;
+}
+// The sequence's span if this kernel takes it, T = 0 if not.
+__device__ __forceinline__ SeqSpan tc_span(const AttnParams& p, int n, unsigned* err) {
+    SeqSpan s = kv_span(p.c, n, err);
+    if (s.T <= 0 || s.T * p.G <= p.rows_lo || s.T * p.G > p.rows_hi) s.T = 0;
+    return s;
+}
+
+// A CTA's current segment: tiles [x, x + cnt) of an item.  Every role walks the same segments.
+struct TcSeg {
+    SeqSpan s;
+    int n, h, rt, x, units, cnt, rts;
+    long long w;
+
+    __device__ __forceinline__ void start(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
+        n = c->n, h = c->h, rt = c->rt, x = c->x, w = c->w0;
+        s = tc_span(p, n, err);
+        rts = (s.T * p.G + kTcRows - 1) / kTcRows;
+        units = tc_units(p, s, rt);
+        cnt = (int)min((long long)(units - x), c->w1 - w);
+    }
+    // Moves on; false when the stretch is done.
+    __device__ __forceinline__ bool next(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
+        w += cnt;
+        if (w >= c->w1) return false;
+        x = 0;
+        if (++rt == rts) {
+            rt = 0;
+            if (++h == p.c.hkv) {
+                h = 0;
+                do s = tc_span(p, ++n, err);
+                while (s.T == 0);
+                rts = (s.T * p.G + kTcRows - 1) / kTcRows;
+            }
+        }
+        units = tc_units(p, s, rt);
+        cnt = (int)min((long long)units, c->w1 - w);
+        return true;
+    }
+    // Tiles [a, b) of this segment that row tile i (0, 1) of the item takes part in, as absolute tile numbers.
+    __device__ __forceinline__ void active(const AttnParams& p, int i, int& a, int& b) const {
+        const int rows = s.T * p.G, r0 = rt * kTcRows + i * kTcTile;
+        int t0, t1;
+        tile_range(p, s, rt * kTcRows, min(rows, (rt + 1) * kTcRows), t0, t1);
+        const int f0 = t0 + x, f1 = f0 + cnt;
+        if (r0 >= rows) {
+            a = b = f0;
+            return;
+        }
+        tile_range(p, s, r0, min(rows, r0 + kTcTile), t0, t1);
+        a = max(t0, f0);
+        b = min(t1, f1);
+        if (b < a) b = a;
+    }
+    __device__ __forceinline__ int first_tile(const AttnParams& p) const {
+        int t0, t1;
+        tile_range(p, s, rt * kTcRows, min(s.T * p.G, (rt + 1) * kTcRows), t0, t1);
+        return t0 + x;
+    }
+    // Whether some row of the item does not see the whole tile.
+    __device__ __forceinline__ bool edge(const AttnParams& p, int tile) const {
+        const int rows = s.T * p.G, base = s.len - s.T, k0 = tile * kTcTile;
+        const int pmin = base + rt * kTcRows / p.G, pmax = base + (min(rows, (rt + 1) * kTcRows) - 1) / p.G;
+        return k0 + kTcTile - 1 > pmin || (p.window > 0 && k0 < pmax - p.window + 1);
+    }
+};
+
+// Shares out the units and finds this CTA's first segment; false: nothing to do.  All threads.
+template <int THREADS>
+__device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, TcScratch* sc, unsigned* err) {
+    const int tid = threadIdx.x, N = p.c.n_seq;
+    int k = 1;  // threads per sequence
+    while (k < 256 && k * 2 * N <= 256) k *= 2;
+    const int per = 256 / k;
+    auto mine_of = [&](int base) {
+        long long mine = 0;
+        const int n = base + tid / k;
+        if (tid < 256 && n < N) {
+            const SeqSpan s = tc_span(p, n, err);
+            const int rts = (s.T * p.G + kTcRows - 1) / kTcRows;
+            for (int rt = tid % k; rt < rts; rt += k) mine += tc_units(p, s, rt);
+        }
+        return mine * p.c.hkv;
+    };
+    long long W = 0, total;
+    for (int base = 0; base < N; base += per) {
+        block_scan<THREADS>(mine_of(base), total, sc->scan);
+        W += total;
+    }
+    const int grid = (int)min((long long)gridDim.x, W), cta = blockIdx.x;
+    if (tid == 0) p.desc[(long long)cta * kDescInts] = -1;
+    if (cta >= grid) return false;
+    const long long w0 = W * cta / grid, w1 = W * (cta + 1) / grid;
+    long long seen = 0;
+    for (int base = 0; base < N; base += per) {
+        const long long before = block_scan<THREADS>(mine_of(base), total, sc->scan);
+        if (seen + total <= w0) {
+            seen += total;
+            continue;
+        }
+        if (tid < 256) sc->pre[tid] = seen + before;
+        if (tid == 0) sc->pre[256] = seen + total;
+        __syncthreads();
+        if (tid < 256 && tid % k == 0 && sc->pre[tid] <= w0 && w0 < sc->pre[tid + k]) {
+            c->n = base + tid / k;
+            c->w0 = sc->pre[tid];        // for now: where the sequence starts
+            c->w1 = sc->pre[tid + k] - sc->pre[tid];
+        }
+        break;
+    }
+    __syncthreads();
+    const int n = c->n;
+    const long long off = w0 - c->w0, per_head = c->w1 / p.c.hkv;
+    const int h = (int)(off / per_head);
+    const long long rem = off - h * per_head;
+    const SeqSpan s = tc_span(p, n, err);
+    const int rts = (s.T * p.G + kTcRows - 1) / kTcRows;
+    long long at = 0;
+    for (int base = 0; base < rts; base += THREADS) {
+        const int rt = base + tid;
+        const int u = rt < rts ? tc_units(p, s, rt) : 0;
+        const long long before = at + block_scan<THREADS>(u, total, sc->scan);
+        if (u > 0 && before <= rem && rem < before + u) {
+            c->rt = rt;
+            c->x = (int)(rem - before);
+        }
+        at += total;
+        if (at > rem) break;
+    }
+    __syncthreads();
+    if (tid == 0) c->h = h, c->W = W, c->w0 = w0, c->w1 = w1;
+    __syncthreads();
+    return true;
+}
+
+template <int D, bool E4M3>
+__global__ void __launch_bounds__(AttnTc<D, E4M3>::THREADS, 1)
+gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const AttnParams p,
+                      unsigned* err) {
+    using namespace sm100;
+    using L = AttnTc<D, E4M3>;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    AttnTcCtl* c = reinterpret_cast<AttnTcCtl*>(smem + L::OFF_CTL);
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    cudaTriggerProgrammaticLaunchCompletion();
+    if (!tc_schedule<L::THREADS>(p, c, reinterpret_cast<TcScratch*>(smem + L::OFF_Q), err)) {
+        cudaGridDependencySynchronize();  // see the end of the kernel
+        return;
+    }
+    if (warp == 1) tmem_alloc(&c->tmem, 512);
+    if (tid == 0) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&c->q_full[i], 128);
+            mbar_init(&c->s_full[i], 1);
+            mbar_init(&c->p_full[i], 128);
+            mbar_init(&c->o_full[i], 1);
+            mbar_init(&c->r_full[i], 1);
+            mbar_init(&c->r_empty[i], 128);
+        }
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&c->k_full[i], E4M3 ? 128 : 1);
+            mbar_init(&c->k_empty[i], 1);
+            mbar_init(&c->v_full[i], 1);
+            mbar_init(&c->v_ready[i], E4M3 ? 128 : 64);
+            mbar_init(&c->v_empty[i], 1);
+            for (int j = 0; j < 4; ++j) c->bad[i][j] = 0;
+        }
+        mbar_init(&c->drain, 1);
+        c->abort_flag = 0;
+        fence_barrier_init();
+        fence_proxy_async();
+    }
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = c->tmem;
+    volatile int* ab = &c->abort_flag;
+
+    if (warp < 4) {
+        reg_dec<E4M3 ? 48 : 56>();
+        if (warp == 0) {
+            // ---- loader.  Fill f of a ring of S stages: stage f % S, waits for the (f / S)-th release.
+            const int npg = kTcTile >> p.c.page_log2, page = 1 << p.c.page_log2;
+            const int boxes = npg * (E4M3 ? 1 : D / 64);
+            const int i = lane % npg, hf = lane / npg;  // this lane's page of the tile and channel half
+            int fk = 0, fv = 0, fr = 0;
+            bool ok = true;
+            TcSeg g;
+            g.start(p, c, err);
+            do {
+                const int t0 = g.first_tile(p);
+                const int32_t* row = p.c.table + (long long)g.n * p.c.max_pages;
+                const int pages = (g.s.len + page - 1) >> p.c.page_log2;
+                auto look = [&](int tile) {  // this lane's page of a tile: -1 behind the sequence's end
+                    const int at = tile * npg + i;
+                    if (lane >= boxes || at >= pages) return -1;
+                    const int pg = row[at];
+                    if (pg >= 0 && pg < p.c.n_pages) return pg;
+                    atomicOr(err, kErrPages);
+                    return 0;
+                };
+                int pg = look(t0);
+                for (int j = 0; ok && j < g.cnt; ++j) {
+                    const int pg_next = j + 1 < g.cnt ? look(t0 + j + 1) : -1;
+                    const int r0 = (pg * p.c.hkv + g.h) << p.c.page_log2;  // < 2^31 (checked on the host)
+                    const uint32_t n = __popc(__ballot_sync(0xffffffffu, pg >= 0));
+#pragma unroll
+                    for (int kv = 0; kv < 2; ++kv) {
+                        if (E4M3) {
+                            const int st = fr % 2;
+                            ok = ok && tc_warp_wait(&c->r_empty[st], ((fr / 2) & 1) ^ 1, ab, err);
+                            if (!ok) break;
+                            if (lane == 0) mbar_expect_tx(&c->r_full[st], n * page * (D + 1));
+                            __syncwarp();
+                            if (pg >= 0) {
+                                const uint8_t* src = static_cast<const uint8_t*>(kv ? p.c.v_cache : p.c.k_cache);
+                                const uint8_t* sc = kv ? p.c.v_scale : p.c.k_scale;
+                                bulk_load(smem + L::OFF_RAW + st * L::RAW + i * page * D, src + (long long)r0 * D, page * D, &c->r_full[st]);
+                                bulk_load(smem + L::OFF_SC + st * kTcTile + i * page, sc + r0, page, &c->r_full[st]);
+                            }
+                            ++fr;
+                        } else {
+                            int& f = kv ? fv : fk;
+                            const int S = kv ? L::NV : L::NK, st = f % S;
+                            uint64_t* full = kv ? &c->v_full[st] : &c->k_full[st];
+                            ok = ok && tc_warp_wait(kv ? &c->v_empty[st] : &c->k_empty[st], ((f / S) & 1) ^ 1, ab, err);
+                            if (!ok) break;
+                            if (lane == 0) mbar_expect_tx(full, n * page * 128);
+                            __syncwarp();
+                            if (pg >= 0)
+                                tma_load_2d(smem + (kv ? L::OFF_V : L::OFF_K) + st * L::TILE + hf * L::HALF + i * page * 128,
+                                            kv ? &tm_v : &tm_k, full, hf * 64, r0);
+                            ++f;
+                        }
+                    }
+                    pg = pg_next;
+                }
+            } while (ok && g.next(p, c, err));
+            if (!ok) {  // given up: let the copies in flight land before the CTA goes (each wait has its own limit)
+                int zero = 0;
+                if (E4M3) {
+                    for (int f = max(0, fr - 2); f < fr; ++f) tc_wait(&c->r_full[f % 2], (f / 2) & 1, &zero, err);
+                } else {
+                    for (int f = max(0, fk - L::NK); f < fk; ++f) tc_wait(&c->k_full[f % L::NK], (f / L::NK) & 1, &zero, err);
+                    for (int f = max(0, fv - L::NV); f < fv; ++f) tc_wait(&c->v_full[f % L::NV], (f / L::NV) & 1, &zero, err);
+                }
+            }
+        } else if (warp == 1) {
+            // ---- MMA issuer (one thread)
+            if (lane == 0) {
+                constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
+                const uint32_t sq = smem_u32(smem + L::OFF_Q), sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
+                int ck = 0, cv = 0, seg = 0;  // K and V tiles taken, segments
+                int np[2] = {0, 0};           // P tiles taken of each row tile
+                bool ok = true;
+                TcSeg g;
+                g.start(p, c, err);
+                do {
+                    const int f0 = g.first_tile(p), f1 = f0 + g.cnt;
+                    int a[2], b[2];
+                    g.active(p, 0, a[0], b[0]);
+                    g.active(p, 1, a[1], b[1]);
+                    for (int i = 0; i < 2; ++i) {
+                        if (ok) ok = tc_wait(&c->q_full[i], seg & 1, ab, err);
+                        // a row tile without tiles here is told so too: no role gets a phase ahead of another
+                        if (ok && b[i] == a[i]) umma_commit(&c->o_full[i]);
+                    }
+                    for (int t = f0; ok && t <= f1; ++t) {
+                        // O_i += P_i V of tile t - 1, then S_i = Q_i K^T of tile t: in issue order, so S may overwrite P
+                        const int stk = ck % L::NK, stv = cv % L::NV;
+                        if (t < f1) ok = ok && tc_wait(&c->k_full[stk], (ck / L::NK) & 1, ab, err);
+                        if (t > f0) ok = ok && tc_wait(&c->v_ready[stv], (cv / L::NV) & 1, ab, err);
+                        for (int i = 0; ok && i < 2; ++i) {
+                            if (t > f0 && t - 1 >= a[i] && t - 1 < b[i]) {
+                                ok = tc_wait(&c->p_full[i], np[i]++ & 1, ab, err);
+                                if (!ok) break;
+                                tc_fence_after();
+#pragma unroll
+                                for (int ks = 0; ks < 8; ++ks)
+                                    umma_bf16_tmem_a(tmem + 256 + i * 128, tmem + i * 128 + ks * 8,
+                                                     desc_mn_sw128(sv + stv * L::TILE + ks * 2048, L::HALF), id_o, t - 1 > a[i] || ks > 0);
+                                if (t == b[i]) umma_commit(&c->o_full[i]);
+                            }
+                            if (t < f1 && t >= a[i] && t < b[i]) {
+                                tc_fence_after();
+#pragma unroll
+                                for (int ks = 0; ks < D / 16; ++ks) {
+                                    const uint32_t off = (ks >> 2) * L::HALF + (ks & 3) * 32;
+                                    umma_bf16(tmem + i * 128, desc_k_sw128(sq + i * L::TILE + off), desc_k_sw128(sk + stk * L::TILE + off), id_s, ks > 0);
+                                }
+                                umma_commit(&c->s_full[i]);
+                            }
+                        }
+                        if (!ok) break;
+                        if (t > f0) {
+                            umma_commit(&c->v_empty[stv]);
+                            ++cv;
+                        }
+                        if (t < f1) {
+                            umma_commit(&c->k_empty[stk]);
+                            ++ck;
+                        }
+                    }
+                    ++seg;
+                } while (ok && g.next(p, c, err));
+                // every MMA has read its operands before the CTA goes
+                umma_commit(&c->drain);
+                int zero = 0;
+                tc_wait(&c->drain, 0, &zero, err);
+            }
+            __syncwarp();
+        } else if (!E4M3) {
+            // ---- V rows that hold a NaN or an infinity, in tiles that are not wholly visible
+            const int t64 = tid - 64;
+            int cv = 0;
+            bool ok = true;
+            TcSeg g;
+            g.start(p, c, err);
+            do {
+                const int f0 = g.first_tile(p);
+                for (int j = 0; ok && j < g.cnt; ++j, ++cv) {
+                    const int st = cv % L::NV;
+                    ok = tc_warp_wait(&c->v_full[st], (cv / L::NV) & 1, ab, err);
+                    if (!ok) break;
+                    if (g.edge(p, f0 + j)) {
+                        uint8_t* v = smem + L::OFF_V + st * L::TILE;
+                        // a thread looks at two rows whole
+#pragma unroll
+                        for (int rr = 0; rr < 2; ++rr) {
+                            const int r = t64 + 64 * rr;
+                            bool bad = false;
+                            for (int ch = 0; ch < D / 8; ++ch) {
+                                const uint4 u = *reinterpret_cast<const uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7));
+                                bad = bad || bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w);
+                            }
+                            if (bad)
+                                for (int ch = 0; ch < D / 8; ++ch)
+                                    *reinterpret_cast<uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
+                            const uint32_t m = __ballot_sync(0xffffffffu, bad);
+                            if (lane == 0) c->bad[st][(r >> 5)] = m;
+                        }
+                        fence_proxy_async();
+                    }
+                    mbar_arrive(&c->v_ready[st]);
+                }
+            } while (ok && g.next(p, c, err));
+        }
+    } else if (warp < 12) {
+        // ---- softmax
+        reg_inc<E4M3 ? 192 : 216>();
+        const int i = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;  // row tile, row in it
+        const uint32_t ts = tmem + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+        const uint32_t to = tmem + 256 + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
+        // a negative scale goes into Q's sign and a zero one into Q itself, so that larger S means larger score
+        const float cs = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
+        const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
+        int ns = 0, no = 0, cv0 = 0;  // S tiles taken, segments done, V tiles before this segment
+        bool ok = true;
+        TcSeg g;
+        g.start(p, c, err);
+        do {
+            const int rows = g.s.T * p.G, row = g.rt * kTcRows + i * kTcTile + r;
+            const bool there = row < rows;
+            const int tok = there ? row / p.G : 0, gh = row - tok * p.G;
+            const int pos = g.s.len - g.s.T + tok;
+            {
+                const uint4* q = reinterpret_cast<const uint4*>(p.q + (long long)(g.s.start + tok) * p.q_stride + (long long)(g.h * p.G + (there ? gh : 0)) * D);
+                uint8_t* dst = smem + L::OFF_Q + i * L::TILE;
+#pragma unroll
+                for (int ch = 0; ch < D / 8; ++ch) {
+                    uint4 u = there ? q[ch] : make_uint4(0, 0, 0, 0);
+                    u.x = (u.x ^ flip) & keep, u.y = (u.y ^ flip) & keep, u.z = (u.z ^ flip) & keep, u.w = (u.w ^ flip) & keep;
+                    *reinterpret_cast<uint4*>(dst + (ch >> 3) * L::HALF + sw128(r, ch & 7)) = u;
+                }
+                fence_proxy_async();
+                mbar_arrive(&c->q_full[i]);
+            }
+            int a, b;
+            g.active(p, i, a, b);
+            const int f0 = g.first_tile(p);
+            // this row tile's own rows: which tiles need masking
+            const int rlo = g.rt * kTcRows + i * kTcTile, rhi = min(rows, rlo + kTcTile) - 1;
+            const int pmin = g.s.len - g.s.T + rlo / p.G, pmax = g.s.len - g.s.T + rhi / p.G;
+            float m = -INFINITY, l = 0.f;
+            for (int t = a; ok && t < b; ++t) {
+                ok = tc_warp_wait(&c->s_full[i], ns & 1, ab, err);
+                if (!ok) break;
+                ++ns;
+                tc_fence_after();
+                float s[4][32];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
+                tmem_wait_ld();
+                const int k0 = t * kTcTile;
+                if (k0 + kTcTile - 1 > pmin || (p.window > 0 && k0 < pmax - p.window + 1)) {
+                    const int chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : -1;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (q * 32 + e > chi || q * 32 + e < clo) s[q][e] = -INFINITY;
+                }
+                float top = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) top = fmaxf(top, s[q][e]);
+                if (__any_sync(0xffffffffu, (top - m) * cs > kRescaleLog2)) {
+                    const float nm = fmaxf(m, top), f = m == -INFINITY ? 0.f : exp2f((m - nm) * cs);
+                    m = nm;
+                    l *= f;
+                    if (t > a) {
+#pragma unroll 1
+                        for (int q = 0; q < D / 16; ++q) {
+                            uint32_t o[16];
+                            tmem_ld16(to + q * 16, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16u(to + q * 16, o);
+                        }
+                    }
+                }
+                const float mc = m == -INFINITY ? 0.f : m * cs;
+                uint32_t bad[4] = {0, 0, 0, 0};
+                int chi = 0, clo = 0;
+                if (g.edge(p, t)) {  // marked keys: see the head of the file
+                    const int cv = cv0 + (t - f0), st = cv % L::NV;
+                    ok = tc_warp_wait(&c->v_ready[st], (cv / L::NV) & 1, ab, err);
+                    if (!ok) break;
+                    chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : 0;
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) bad[q] = c->bad[st][q];
+                }
+                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    uint32_t w[16];
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        const float x = ex2_approx(fmaf(s[q][e], cs, -mc)), y = ex2_approx(fmaf(s[q][e + 1], cs, -mc));
+                        l4[(e >> 1) & 3] += x + y;
+                        w[e >> 1] = pack_bf16x2(x, y);
+                    }
+                    if (bad[q]) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (((bad[q] >> e) & 1) && q * 32 + e <= chi && q * 32 + e >= clo)
+                                w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0x7fc00000u : (w[e >> 1] & 0xffff0000u) | 0x7fc0u;
+                    }
+                    __syncwarp();
+                    tmem_st16u(ts + q * 16, w);
+                }
+                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                tmem_wait_st();
+                tc_fence_before();
+                mbar_arrive(&c->p_full[i]);
+            }
+            cv0 += g.cnt;
+            if (!ok) break;
+            // ---- the segment's result
+            ok = tc_warp_wait(&c->o_full[i], no & 1, ab, err);
+            if (!ok) break;
+            ++no;
+            tc_fence_after();
+            const bool whole = g.cnt == g.units;
+            const int slot = g.w == c->w0 ? 0 : 1;
+            const long long part = ((long long)blockIdx.x * 2 + slot) * kTcRows + i * kTcTile + r;
+            const long long at = (long long)(g.s.start + tok) * p.hq + g.h * p.G + gh;
+            if (there) {
+                const float m2 = m == -INFINITY ? -INFINITY : m * cs;
+                if (whole) {
+                    if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+                } else {
+                    p.ml[part * 2] = m2;
+                    p.ml[part * 2 + 1] = l;
+                }
+            }
+            if (b > a) {
+                const float inv = whole ? (l == 0.f ? 0.f : 1.f / l) : 1.f;
+#pragma unroll
+                for (int q = 0; q < D / 32; ++q) {
+                    float o[32];
+                    tmem_ld32(to + q * 32, o);
+                    tmem_wait_ld();
+                    if (there) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] *= inv;
+                        if (whole && !p.o_f32) {
+                            uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(p.o) + at * D + q * 32);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e)
+                                dst[e] = make_uint4(pack_bf16x2(o[8 * e], o[8 * e + 1]), pack_bf16x2(o[8 * e + 2], o[8 * e + 3]),
+                                                    pack_bf16x2(o[8 * e + 4], o[8 * e + 5]), pack_bf16x2(o[8 * e + 6], o[8 * e + 7]));
+                        } else {
+                            float4* dst = reinterpret_cast<float4*>((whole ? static_cast<float*>(p.o) + at * D : p.part + part * D) + q * 32);
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) dst[e] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                        }
+                    }
+                }
+                tc_fence_before();  // O is free once the next Q (arrived after this) lets the issuer go on
+            }
+            if (!whole && g.x == 0 && i == 0 && r == 0) {  // the item starts here and ends in a later CTA
+                const long long grid = min((long long)gridDim.x, c->W), end = g.w + g.units;
+                int* desc = p.desc + (long long)blockIdx.x * kDescInts;
+                desc[0] = g.n;
+                desc[1] = g.h;
+                desc[2] = g.rt * kTcRows;
+                desc[3] = min(kTcRows, rows - g.rt * kTcRows);
+                desc[4] = slot;
+                desc[5] = (int)((end * grid + c->W - 1) / c->W) - (int)blockIdx.x;
+                desc[6] = g.s.start;
+            }
+        } while (ok && g.next(p, c, err));
+    } else {
+        // ---- 8-bit cache: codes to bf16.  Eight (D = 64: four) threads share a row, 16 codes each.
+        reg_dec<80>();
+        const int t128 = tid - 384;
+        constexpr int TPR = D / 16, RPP = 128 / TPR;  // threads of a row, rows per pass
+        const int col = t128 % TPR, r_in = t128 / TPR;
+        int fr = 0, fk = 0, fv = 0;
+        bool ok = true;
+        TcSeg g;
+        g.start(p, c, err);
+        do {
+            const int f0 = g.first_tile(p);
+            for (int j = 0; ok && j < g.cnt; ++j) {
+                const bool edge = g.edge(p, f0 + j);
+                const int valid = g.s.len - (f0 + j) * kTcTile;  // rows of the tile that are positions at all
+#pragma unroll 1
+                for (int kv = 0; kv < 2; ++kv) {
+                    const int rs = fr % 2;
+                    int& f = kv ? fv : fk;
+                    const int S = kv ? L::NV : L::NK, st = f % S;
+                    ok = tc_warp_wait(&c->r_full[rs], (fr / 2) & 1, ab, err) &&
+                         tc_warp_wait(kv ? &c->v_empty[st] : &c->k_empty[st], ((f / S) & 1) ^ 1, ab, err);
+                    if (!ok) break;
+                    const uint8_t* raw = smem + L::OFF_RAW + rs * L::RAW;
+                    const uint8_t* sc = smem + L::OFF_SC + rs * kTcTile;
+                    uint8_t* dst = smem + (kv ? L::OFF_V : L::OFF_K) + st * L::TILE;
+#pragma unroll 4
+                    for (int pass = 0; pass < TPR; ++pass) {
+                        const int r = pass * RPP + r_in;
+                        const uint4 u = *reinterpret_cast<const uint4*>(raw + r * D + col * 16);
+                        unsigned byte = sc[r];
+                        // a value row that may be masked must be finite: one with the NaN scale is zeroed and marked
+                        bool bad = false;
+                        if (kv && edge) {
+                            bad = byte == kScaleNan && r < valid;
+                            if (byte == kScaleNan || r >= valid) byte = 0;
+                            const uint32_t hit = __ballot_sync(0xffffffffu, bad);
+                            // the warp covers 32 / TPR neighbouring rows
+                            uint32_t mark = 0;
+#pragma unroll
+                            for (int q = 0; q < 32 / TPR; ++q) mark |= ((hit >> (q * TPR)) & 1u) << q;
+                            constexpr int RW = 32 / TPR;
+                            uint8_t* bytes = reinterpret_cast<uint8_t*>(c->bad[st]);
+                            // RW = 4 or 8 rows: a nibble or a byte of the mask
+                            const int r0 = pass * RPP + (t128 >> 5) * RW;
+                            if (RW == 8) {
+                                if (lane == 0) bytes[r0 >> 3] = (uint8_t)mark;
+                            } else if (lane == 0) {
+                                // clear and set this nibble (its neighbour belongs to another warp)
+                                atomicAnd(&c->bad[st][r0 >> 5], ~(0xfu << (r0 & 31)));
+                                atomicOr(&c->bad[st][r0 >> 5], mark << (r0 & 31));
+                            }
+                        }
+                        // 2^(byte - 127) as bf16: the byte is its exponent field (0 clears the row, 255 is NaN)
+                        const uint32_t s1 = byte == kScaleNan ? 0x7fc0u : byte << 7, s2 = s1 | (s1 << 16);
+                        const uint32_t cw[4] = {u.x, u.y, u.z, u.w};
+                        uint32_t o[8];
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            o[2 * q] = mul_bf16x2(e4m3_pair(cw[q], 0), s2);
+                            o[2 * q + 1] = mul_bf16x2(e4m3_pair(cw[q], 1), s2);
+                        }
+                        uint8_t* line = dst + (col >> 2) * L::HALF;
+                        *reinterpret_cast<uint4*>(line + sw128(r, (2 * col) & 7)) = make_uint4(o[0], o[1], o[2], o[3]);
+                        *reinterpret_cast<uint4*>(line + sw128(r, (2 * col + 1) & 7)) = make_uint4(o[4], o[5], o[6], o[7]);
+                    }
+                    fence_proxy_async();
+                    mbar_arrive(&c->r_empty[rs]);
+                    mbar_arrive(kv ? &c->v_ready[st] : &c->k_full[st]);
+                    ++fr;
+                    ++f;
+                }
+            }
+        } while (ok && g.next(p, c, err));
+    }
+    __syncthreads();
+    if (warp == 1) {
+        __syncwarp();
+        tmem_relinquish();
+        tmem_dealloc(tmem, 512);
+    }
+    // with a decode kernel before this one on the stream: its results are complete when this kernel is
+    cudaGridDependencySynchronize();
+}
+
+// 2-D map over the cache's rows [n_pages * hkv * page][d], box 64 channels x one page, 128-byte swizzle.
+typedef CUresult (*AttnEncodeTiled)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                    const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+inline bool make_cache_map(CUtensorMap* map, const void* base, int d, long long rows, int page) {
+    static const AttnEncodeTiled enc = [] {
+        void* ptr = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+            q != cudaDriverEntryPointSuccess)
+            ptr = nullptr;
+        return reinterpret_cast<AttnEncodeTiled>(ptr);
+    }();
+    if (!enc) return false;
+    const cuuint64_t dims[2] = {(cuuint64_t)d, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)d * 2};
+    const cuuint32_t box[2] = {64, (cuuint32_t)page};
+    const cuuint32_t estr[2] = {1, 1};
+    return enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(base), dims, strides, box, estr,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+}  // namespace gdn
