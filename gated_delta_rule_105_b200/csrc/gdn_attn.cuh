@@ -92,6 +92,14 @@ __device__ __forceinline__ long long block_scan(long long v, long long& total, l
     return before + x - v;
 }
 
+__device__ __forceinline__ void attn_store4(void* o, int f32, long long at, float4 a, float f) {
+    if (f32) *reinterpret_cast<float4*>(static_cast<float*>(o) + at) = make_float4(a.x * f, a.y * f, a.z * f, a.w * f);
+    else *reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(o) + at) = make_uint2(pack_bf16x2(a.x * f, a.y * f), pack_bf16x2(a.z * f, a.w * f));
+}
+__device__ __forceinline__ float attn_lse(float m, float l) {
+    return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.6931471805599453f;
+}
+
 // ------------------------------------------------------------------------------------------ few rows
 // mma.sync kernel for up to 16 query rows per item.  Bound by the cache's bytes: tensor work is small, and what counts
 // is that every warp keeps 16-byte loads in flight.  K and V go from global memory straight into the registers of
@@ -112,36 +120,54 @@ __device__ __forceinline__ uint32_t mul_bf16x2(uint32_t a, uint32_t b) {
     asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
     return r;
 }
-// e4m3 codes in the high bytes of both halves of `w` (low bytes: anything) as a bf16 pair.  The code's exponent and
-// mantissa moved to bf16's place make the value times 2^-120 (biases 7 and 127), subnormal codes included, and one
-// exact multiplication undoes that.  0x7f, e4m3's NaN, would read as 480: the cache writer never stores it.
-__device__ __forceinline__ uint32_t e4m3_hi_to_bf16x2(uint32_t w) {
-    const uint32_t s = w & 0x80008000u;
-    return mul_bf16x2(((w >> 4) & 0x07f007f0u) | s, 0x7b807b80u);
+// prmt in its default mode: selector nibbles of 8 and above give eight copies of the byte's sign bit (__byte_perm takes
+// three bits of each nibble only).
+__device__ __forceinline__ uint32_t permute(uint32_t a, uint32_t b, uint32_t sel) {
+    uint32_t r;
+    asm("prmt.b32 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(sel));
+    return r;
 }
-// Codes 0, 1 and 2, 3 of a word.
+// Two e4m3 codes a and b, each below a byte of its own sign (`w` = code a, sign a, code b, sign b from low to high, one
+// byte permute with sign replication), as a bf16 pair.  Shifted left by 4 and masked, sign, exponent and mantissa stand
+// where bf16 has them; the biases (7 and 127) make that the value times 2^-120, subnormal codes included, and one exact
+// multiplication undoes it.  0x7f, e4m3's NaN, would read as 480: the cache writer never stores it.
+__device__ __forceinline__ uint32_t e4m3_signed_to_bf16x2(uint32_t w) {
+    return mul_bf16x2((w << 4) & 0x87f087f0u, 0x7b807b80u);
+}
+// Codes 0, 1 or 2, 3 of a word.
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, int hi) {
-    return e4m3_hi_to_bf16x2(hi ? __byte_perm(w, 0, 0x3424) : __byte_perm(w, 0, 0x1404));
+    return e4m3_signed_to_bf16x2(permute(w, 0, hi ? 0xb3a2 : 0x9180));
+}
+__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                         uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-constexpr int kDecThreads = 256, kDecWarps = 8, kDecRows = 16;
+constexpr int kDecThreads = 256, kDecWarps = 8;
 constexpr float kRescaleLog2 = 8.f;  // the running maximum follows only when it would be off by more than 2^8
 
-template <int D, bool E4M3> struct DecTraits {
-    static constexpr int KS = (D == 128 && !E4M3) ? 16 : 32;  // keys of one warp step
+template <int D, bool E4M3, int R> struct DecTraits {
+    static constexpr int KS = D == 128 ? 16 : 32;       // keys of one warp step
     static constexpr int UNIT = KS * kDecWarps;
-    static constexpr int KL = D * (E4M3 ? 1 : 2) / 64;        // 16-byte K loads per thread and 8 keys
-    static constexpr int MT = D / 16;                         // channel tiles of 16
-    static constexpr size_t smem = kDecWarps * kDecRows * D * 4 + kDecWarps * kDecRows * 8 + 256;
+    static constexpr int KL = D * (E4M3 ? 1 : 2) / 64;  // 16-byte K loads per thread and 8 keys
+    static constexpr int MT = D / 16;                   // channel tiles of 16
+    static constexpr int RS = R / 8;                    // sets of 8 rows
+    static constexpr int QF = E4M3 ? D / 32 : D / 16;   // k-steps
+    static constexpr int CTAS = R == 8 && (E4M3 || D == 64) ? 2 : 1;  // per SM
+    static constexpr size_t smem = kDecWarps * R * D * 4 + kDecWarps * R * 8 + 256;
 };
 
-template <int D, bool E4M3>
-__global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
-    using Tr = DecTraits<D, E4M3>;
-    constexpr int KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, R = kDecRows, NT = KS / 8, KG = KS / 16;
+template <int D, bool E4M3, int R>
+__global__ void __launch_bounds__(kDecThreads, (DecTraits<D, E4M3, R>::CTAS))
+gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
+    using Tr = DecTraits<D, E4M3, R>;
+    constexpr int KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS, QF = Tr::QF, NT = KS / 8, KG = KS / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     float* s_o = reinterpret_cast<float*>(smem);                  // [warps][R][D]
     float* s_ml = s_o + kDecWarps * R * D;                        // [warps][R][2]
@@ -198,10 +224,15 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
 
         // ---- the item's query rows: A fragments, in K's channel order
         const int row_lo = rg * R + g, rows = T * p.G;
-        uint32_t qf[D / 16][4];
-        int hi_[2], lo_[2];  // keys [lo_, hi_] that rows g and g + 8 see
+        // bf16 cache: a0, a2 of rows g and (R = 16) a1, a3 of rows g + 8.  8-bit cache: the row as q = 2^e (q1 + q2 / 16),
+        // two e4m3 rows with e per row: q1 takes 4 of bf16's 8 significant bits and q2 the exact rest, down to 2^-22 of
+        // the row's largest; so K's codes go into the matrix instruction as they are, without conversion, at twice
+        // bf16's rate.  R = 8: q1 in rows g and q2 in rows g + 8 of one fragment; R = 16: qf is q1 and qg is q2 of both.
+        uint32_t qf[QF][4], qg[E4M3 && R == 16 ? QF : 1][4];
+        float qscale[RS];
+        int hi_[RS], lo_[RS];  // keys [lo_, hi_] that rows g and g + 8 see
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RS; ++r) {
             const int row = row_lo + 8 * r;
             const bool there = row < rows;
             const int tok = there ? row / p.G : 0, gh = there ? row - tok * p.G : 0;
@@ -209,14 +240,51 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
             hi_[r] = there ? pos : -1;
             lo_[r] = p.window > 0 ? pos - p.window + 1 : 0;
             const __nv_bfloat16* q = p.q + (long long)(sp.s.start + tok) * p.q_stride + (h * p.G + gh) * D;
+            qscale[r] = p.scale_log2;
             if (E4M3) {
+                // word s of a thread's 16 channels 64 j + 16 t is k-index 4t.. of half s & 1 of k-step 2 j + s / 2
+                uint2 u[D / 64][4];
+                unsigned top = 0;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        const uint2 u = there ? *reinterpret_cast<const uint2*>(q + 64 * j + 16 * t + 4 * s) : make_uint2(0, 0);
-                        qf[4 * j + s][r] = u.x;
-                        qf[4 * j + s][2 + r] = u.y;
+                        u[j][s] = there ? *reinterpret_cast<const uint2*>(q + 64 * j + 16 * t + 4 * s) : make_uint2(0, 0);
+                        top = max(max(top, u[j][s].x & 0x7fffu), (u[j][s].x >> 16) & 0x7fffu);
+                        top = max(max(top, u[j][s].y & 0x7fffu), (u[j][s].y >> 16) & 0x7fffu);
+                    }
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const bool bad = top >= 0x7f80u;  // an infinity or a NaN: the row's scores are NaN
+                int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
+                e = min(max(e, kScaleExpMin), kScaleExpMax);
+                const float inv = __int_as_float((127 - e) << 23);
+                qscale[r] = bad ? __int_as_float(0x7fc00000) : p.scale_log2 * __int_as_float((127 + e) << 23);
+#pragma unroll
+                for (int j = 0; j < D / 64; ++j)
+#pragma unroll
+                    for (int s = 0; s < 4; ++s) {
+                        float x[4] = {__uint_as_float(u[j][s].x << 16), __uint_as_float(u[j][s].x & 0xffff0000u),
+                                      __uint_as_float(u[j][s].y << 16), __uint_as_float(u[j][s].y & 0xffff0000u)};
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) x[i] = bad ? 0.f : x[i] * inv;
+                        const uint32_t c1 = pack_e4m3x4(x[0], x[1], x[2], x[3]);
+                        float y[4];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c1 >> (16 * i)), __NV_E4M3);
+                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
+                            y[2 * i] = f.x, y[2 * i + 1] = f.y;
+                        }
+                        const uint32_t c2 = pack_e4m3x4((x[0] - y[0]) * 16.f, (x[1] - y[1]) * 16.f, (x[2] - y[2]) * 16.f, (x[3] - y[3]) * 16.f);
+                        const int ks = 2 * j + (s >> 1), at = 2 * (s & 1);
+                        if (R == 8) {
+                            qf[ks][at] = c1;
+                            qf[ks][at + 1] = c2;
+                        } else {
+                            qf[ks][at + r] = c1;
+                            qg[ks][at + r] = c2;
+                        }
                     }
             } else {
 #pragma unroll
@@ -226,52 +294,54 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
                     qf[2 * j][2 + r] = u.y;
                     qf[2 * j + 1][r] = u.z;
                     qf[2 * j + 1][2 + r] = u.w;
+                    if (R == 8) qf[2 * j][1] = qf[2 * j][3] = qf[2 * j + 1][1] = qf[2 * j + 1][3] = 0;
                 }
             }
         }
         // keys that every row of the sequence sees: [full_lo, full_hi]
         const int full_hi = len - T, full_lo = p.window > 0 ? len - p.window : 0;
 
-        float o[2][MT][4] = {};
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+        float o[RS][MT][4] = {};
+        float m[RS], l[RS];
+#pragma unroll
+        for (int r = 0; r < RS; ++r) m[r] = -INFINITY, l[r] = 0.f;
         const int k_begin = (sp.u_first + x0) * UNIT + warp * KS;
         uint4 kr[NT][KL];
-        uint4 vr[KG][4];        // bf16, D == 128: two chunks -> vr2
-        uint4 vr2[KG][4];
-        unsigned ksc[NT], vsc[NT];  // scale bytes of keys 2t, 2t + 1 of each 8
+        uint4 vr[KG][4];
+        uint4 vr2[!E4M3 && D == 128 ? KG : 1][4];  // channels 64.. of a bf16 row of 128
+        unsigned ksc[NT], vsc[NT];                 // scale bytes of keys 2t, 2t + 1 of each 8
         constexpr int ESZ = E4M3 ? 1 : 2;
 
-        auto page_row = [&](int k0) {  // row index of position k0 (a multiple of 16) in the pool
-            const int kk = min(k0, len - 1) & ~15;
-            int pg = p.c.table[(long long)n * p.c.max_pages + (kk >> p.c.page_log2)];
-            if (pg < 0 || pg >= p.c.n_pages) {
-                if (lane == 0) atomicOr(err, kErrPages);
-                pg = 0;
-            }
-            return (((long long)pg * p.c.hkv + h) << p.c.page_log2) + (kk & ((1 << p.c.page_log2) - 1));
-        };
-        long long prow[KG];
+        const int32_t* table = p.c.table + (long long)n * p.c.max_pages;
+        int prow[KG];  // row of the step's 16-key groups in the pool (below 2^31: checked on the host)
         auto find = [&](int k0) {
 #pragma unroll
-            for (int kg = 0; kg < KG; ++kg) prow[kg] = page_row(k0 + 16 * kg);
+            for (int kg = 0; kg < KG; ++kg) {
+                const int kk = min(k0 + 16 * kg, (len - 1) & ~15);
+                int pg = table[kk >> p.c.page_log2];
+                if ((unsigned)pg >= (unsigned)p.c.n_pages) {
+                    if (lane == 0) atomicOr(err, kErrPages);
+                    pg = 0;
+                }
+                prow[kg] = ((pg * p.c.hkv + h) << p.c.page_log2) + (kk & ((1 << p.c.page_log2) - 1));
+            }
         };
         auto load_k = [&]() {
 #pragma unroll
             for (int kt = 0; kt < NT; ++kt) {
-                const long long row = prow[kt >> 1] + 8 * (kt & 1);
-                const uint8_t* base = static_cast<const uint8_t*>(p.c.k_cache) + (row + g) * (D * ESZ) + 16 * t;
+                const uint8_t* base = static_cast<const uint8_t*>(p.c.k_cache) + (long long)(prow[kt >> 1] + g) * (D * ESZ) + 16 * t + 8 * (kt & 1) * D * ESZ;
 #pragma unroll
                 for (int j = 0; j < KL; ++j) kr[kt][j] = *reinterpret_cast<const uint4*>(base + 64 * j);
-                if (E4M3) ksc[kt] = *reinterpret_cast<const uint16_t*>(p.c.k_scale + row + 2 * t);
+                if (E4M3) ksc[kt] = *reinterpret_cast<const uint16_t*>(p.c.k_scale + prow[kt >> 1] + 2 * t + 8 * (kt & 1));
             }
         };
-        auto load_v = [&]() {
+        auto load_v = [&](const int (&row)[KG]) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
+                const uint8_t* at = static_cast<const uint8_t*>(p.c.v_cache) + (long long)(row[kg] + 2 * t) * (D * ESZ);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const long long row = prow[kg] + 2 * t + (i & 1) + 8 * (i >> 1);
-                    const uint8_t* base = static_cast<const uint8_t*>(p.c.v_cache) + row * (D * ESZ);
+                    const uint8_t* base = at + ((i & 1) + 8 * (i >> 1)) * D * ESZ;
                     if (E4M3 && D == 64) {
                         const uint2 u = *reinterpret_cast<const uint2*>(base + 8 * g);
                         vr[kg][i] = make_uint4(u.x, u.y, 0, 0);
@@ -281,47 +351,62 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
                     if (!E4M3 && D == 128) vr2[kg][i] = *reinterpret_cast<const uint4*>(base + 128 + 16 * g);
                 }
                 if (E4M3) {
-                    vsc[2 * kg] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 2 * t);
-                    vsc[2 * kg + 1] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 8 + 2 * t);
+                    vsc[2 * kg] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + row[kg] + 2 * t);
+                    vsc[2 * kg + 1] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + row[kg] + 8 + 2 * t);
                 }
             }
         };
         find(k_begin);
         load_k();
-        load_v();
+        load_v(prow);
+        find(k_begin + UNIT);
 
         for (int x = 0; x < cnt; ++x) {
             const int k0 = k_begin + x * UNIT;
-            const bool more = x + 1 < cnt;
             // ---- scores
-            float s[NT][4];
+            float s[NT][2 * RS];
 #pragma unroll
             for (int kt = 0; kt < NT; ++kt) {
-                s[kt][0] = s[kt][1] = s[kt][2] = s[kt][3] = 0.f;
+                float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < KL; ++j) {
                     const uint32_t kw[4] = {kr[kt][j].x, kr[kt][j].y, kr[kt][j].z, kr[kt][j].w};
-                    if (E4M3) {
 #pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            mma_bf16(s[kt], qf[4 * j + i][0], qf[4 * j + i][1], qf[4 * j + i][2], qf[4 * j + i][3],
-                                     e4m3_pair(kw[i], 0), e4m3_pair(kw[i], 1));
-                    } else {
-#pragma unroll
-                        for (int i = 0; i < 2; ++i)
-                            mma_bf16(s[kt], qf[2 * j + i][0], qf[2 * j + i][1], qf[2 * j + i][2], qf[2 * j + i][3],
-                                     kw[2 * i], kw[2 * i + 1]);
+                    for (int i = 0; i < 2; ++i) {
+                        const uint32_t(&a)[4] = qf[2 * j + i];
+                        if (E4M3) {
+                            mma_e4m3(c, a[0], a[1], a[2], a[3], kw[2 * i], kw[2 * i + 1]);
+                            if (R == 16) {
+                                const uint32_t(&b)[4] = qg[(R == 16 && E4M3) ? 2 * j + i : 0];
+                                mma_e4m3(c2, b[0], b[1], b[2], b[3], kw[2 * i], kw[2 * i + 1]);
+                            }
+                        } else {
+                            mma_bf16(c, a[0], a[1], a[2], a[3], kw[2 * i], kw[2 * i + 1]);
+                        }
                     }
                 }
-                const float c0 = E4M3 ? p.scale_log2 * kv_scale_value(ksc[kt] & 0xff) : p.scale_log2;
-                const float c1 = E4M3 ? p.scale_log2 * kv_scale_value(ksc[kt] >> 8) : p.scale_log2;
-                s[kt][0] *= c0, s[kt][1] *= c1, s[kt][2] *= c0, s[kt][3] *= c1;
+                if (E4M3) {
+                    const float k0s = kv_scale_value(ksc[kt] & 0xff), k1s = kv_scale_value(ksc[kt] >> 8);
+                    if (R == 8) {
+                        s[kt][0] = fmaf(c[2], 0.0625f, c[0]) * (qscale[0] * k0s);
+                        s[kt][1] = fmaf(c[3], 0.0625f, c[1]) * (qscale[0] * k1s);
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2 * RS; ++i)
+                            s[kt][i] = fmaf(c2[i], 0.0625f, c[i]) * (qscale[i >> 1] * ((i & 1) ? k1s : k0s));
+                    }
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * p.scale_log2;
+                }
             }
-            // ---- the next step's keys
-            if (more) {
-                // V of this step is in registers already; prow moves on
-                find(k0 + UNIT);
+            // ---- the next step's keys, and where the one after that lies
+            int vrow[KG];
+#pragma unroll
+            for (int kg = 0; kg < KG; ++kg) vrow[kg] = prow[kg];
+            if (x + 1 < cnt) {
                 load_k();
+                find(k0 + 2 * UNIT);
             }
             // ---- mask: only steps that some row does not see whole
             const bool edge = k0 < full_lo || k0 + KS - 1 > full_hi;
@@ -329,22 +414,25 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
 #pragma unroll
                 for (int kt = 0; kt < NT; ++kt)
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const int key = k0 + 8 * kt + 2 * t + (i & 1), r = i >> 1;
-                        if (key > hi_[r] || key < lo_[r]) s[kt][i] = -INFINITY;
+                    for (int i = 0; i < 2 * RS; ++i) {
+                        const int key = k0 + 8 * kt + 2 * t + (i & 1);
+                        if (key > hi_[i >> 1] || key < lo_[i >> 1]) s[kt][i] = -INFINITY;
                     }
             }
             // ---- running maximum
-            float top[2] = {-INFINITY, -INFINITY};
+            float top[RS];
+            bool grow = false;
 #pragma unroll
-            for (int kt = 0; kt < NT; ++kt) {
-                top[0] = fmaxf(top[0], fmaxf(s[kt][0], s[kt][1]));
-                top[1] = fmaxf(top[1], fmaxf(s[kt][2], s[kt][3]));
+            for (int r = 0; r < RS; ++r) {
+                top[r] = -INFINITY;
+#pragma unroll
+                for (int kt = 0; kt < NT; ++kt) top[r] = fmaxf(top[r], fmaxf(s[kt][2 * r], s[kt][2 * r + 1]));
+                grow = grow || top[r] > m[r] + kRescaleLog2;
             }
-            if (__any_sync(0xffffffffu, top[0] > m[0] + kRescaleLog2 || top[1] > m[1] + kRescaleLog2)) {
-                float f[2];
+            if (__any_sync(0xffffffffu, grow)) {
+                float f[RS];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < RS; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
                     const float nm = fmaxf(m[r], top[r]);
@@ -353,7 +441,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
                     m[r] = nm;
                 }
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
+                for (int r = 0; r < RS; ++r) {
                     const float fa = __shfl_sync(0xffffffffu, f[r], 8 * t), fb = __shfl_sync(0xffffffffu, f[r], 8 * t + 4);
 #pragma unroll
                     for (int i = 0; i < MT; ++i) {
@@ -362,19 +450,18 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
                     }
                 }
             }
-            const float mu[2] = {m[0] == -INFINITY ? 0.f : m[0], m[1] == -INFINITY ? 0.f : m[1]};
-            uint32_t pf[NT][2];  // P^T fragments: rows g and g + 8, keys 2t, 2t + 1 of each 8
+            uint32_t pf[NT][RS];  // P^T fragments: rows g and g + 8, keys 2t, 2t + 1 of each 8
 #pragma unroll
-            for (int kt = 0; kt < NT; ++kt) {
+            for (int r = 0; r < RS; ++r) {
+                const float mu = m[r] == -INFINITY ? 0.f : m[r];
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float a = sm100::ex2_approx(s[kt][2 * r] - mu[r]), b = sm100::ex2_approx(s[kt][2 * r + 1] - mu[r]);
+                for (int kt = 0; kt < NT; ++kt) {
+                    float a = sm100::ex2_approx(s[kt][2 * r] - mu), b = sm100::ex2_approx(s[kt][2 * r + 1] - mu);
                     l[r] += a + b;
                     if (E4M3) {
-                        const float va = kv_scale_value(vsc[kt] & 0xff), vb = kv_scale_value(vsc[kt] >> 8);
                         // a key that this row does not see adds nothing, whatever its scale says
-                        a = edge && s[kt][2 * r] == -INFINITY ? 0.f : a * va;
-                        b = edge && s[kt][2 * r + 1] == -INFINITY ? 0.f : b * vb;
+                        a = edge && s[kt][2 * r] == -INFINITY ? 0.f : a * kv_scale_value(vsc[kt] & 0xff);
+                        b = edge && s[kt][2 * r + 1] == -INFINITY ? 0.f : b * kv_scale_value(vsc[kt] >> 8);
                     }
                     pf[kt][r] = pack_bf16x2(a, b);
                 }
@@ -401,7 +488,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
                             if (D == 128) vr2[kg][i] = make_uint4(0, 0, 0, 0);
                             const int kt = 2 * kg + (i >> 1), key = k0 + 8 * kt + 2 * t + (i & 1);
 #pragma unroll
-                            for (int r = 0; r < 2; ++r)
+                            for (int r = 0; r < RS; ++r)
                                 if (key <= hi_[r] && key >= lo_[r])
                                     pf[kt][r] = (i & 1) ? (pf[kt][r] & 0xffffu) | 0x7fc00000u : (pf[kt][r] & 0xffff0000u) | 0x7fc0u;
                         }
@@ -410,40 +497,39 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
             // ---- O^T += V^T P^T
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
-                const uint32_t b00 = pf[2 * kg][0], b01 = pf[2 * kg + 1][0], b10 = pf[2 * kg][1], b11 = pf[2 * kg + 1][1];
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     uint32_t a0, a1, a2, a3;
                     if (E4M3) {
-                        // channels 2i, 2i + 1 of this thread's 16 (8): codes of both keys of a pair into one word
+                        // channels 2i, 2i + 1 of this thread's 16 (8): codes of both keys of a pair, each with its sign
                         const int wd = i >> 1;
                         auto word = [&](const uint4& u) { return wd == 0 ? u.x : wd == 1 ? u.y : wd == 2 ? u.z : u.w; };
                         const uint32_t x0 = word(vr[kg][0]), x1 = word(vr[kg][1]), x2 = word(vr[kg][2]), x3 = word(vr[kg][3]);
-                        const unsigned sa = (i & 1) ? 0x6020 : 0x4000, sb = (i & 1) ? 0x7030 : 0x5010;
-                        a0 = e4m3_hi_to_bf16x2(__byte_perm(x0, x1, sa));
-                        a1 = e4m3_hi_to_bf16x2(__byte_perm(x0, x1, sb));
-                        a2 = e4m3_hi_to_bf16x2(__byte_perm(x2, x3, sa));
-                        a3 = e4m3_hi_to_bf16x2(__byte_perm(x2, x3, sb));
+                        const unsigned sa = (i & 1) ? 0xe6a2 : 0xc480, sb = (i & 1) ? 0xf7b3 : 0xd591;
+                        a0 = e4m3_signed_to_bf16x2(permute(x0, x1, sa));
+                        a1 = e4m3_signed_to_bf16x2(permute(x0, x1, sb));
+                        a2 = e4m3_signed_to_bf16x2(permute(x2, x3, sa));
+                        a3 = e4m3_signed_to_bf16x2(permute(x2, x3, sb));
                     } else {
                         const int wd = i & 3;
                         auto word = [&](const uint4& u) { return wd == 0 ? u.x : wd == 1 ? u.y : wd == 2 ? u.z : u.w; };
-                        const uint4(&vv)[4] = i < 4 ? vr[kg] : vr2[kg];
+                        const uint4(&vv)[4] = i < 4 ? vr[kg] : vr2[D == 128 ? kg : 0];
                         const uint32_t x0 = word(vv[0]), x1 = word(vv[1]), x2 = word(vv[2]), x3 = word(vv[3]);
                         a0 = __byte_perm(x0, x1, 0x5410);
                         a1 = __byte_perm(x0, x1, 0x7632);
                         a2 = __byte_perm(x2, x3, 0x5410);
                         a3 = __byte_perm(x2, x3, 0x7632);
                     }
-                    mma_bf16(o[0][i], a0, a1, a2, a3, b00, b01);
-                    mma_bf16(o[1][i], a0, a1, a2, a3, b10, b11);
+#pragma unroll
+                    for (int r = 0; r < RS; ++r) mma_bf16(o[r][i], a0, a1, a2, a3, pf[2 * kg][r], pf[2 * kg + 1][r]);
                 }
             }
-            if (more) load_v();
+            if (x + 1 < cnt) load_v(vrow);
         }
 
         // ---- join the warps
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RS; ++r) {
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
             l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
             if (t == 0) {
@@ -453,7 +539,7 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
         }
         __syncthreads();
 #pragma unroll
-        for (int r = 0; r < 2; ++r) {
+        for (int r = 0; r < RS; ++r) {
             float f[2];
 #pragma unroll
             for (int c = 0; c < 2; ++c) {
@@ -493,14 +579,8 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
             if (whole) {
                 const int tok = row / p.G, gh = row - tok * p.G;
                 const long long at = (long long)(sp.s.start + tok) * p.hq + h * p.G + gh;
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
-                if (p.o_f32) {
-                    reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * D)[d / 4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-                } else {
-                    reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * D)[d / 4] =
-                        make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-                }
-                if (d == 0 && p.lse) p.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+                attn_store4(p.o, p.o_f32, at * D + d, a, ll == 0.f ? 0.f : 1.f / ll);
+                if (d == 0 && p.lse) p.lse[at] = attn_lse(mm, ll);
             } else {
                 const long long at = ((long long)cta * 2 + slot) * R + r;
                 reinterpret_cast<float4*>(p.part + at * D)[d / 4] = a;
@@ -512,13 +592,12 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
         }
         if (!whole && x0 == 0 && tid == 0) {  // the item starts here and ends in a later CTA
             const long long end = w + sp.units;
-            const int c1 = (int)((end * grid + W - 1) / W);  // first CTA whose stretch begins at `end` or behind
             desc[0] = n;
             desc[1] = h;
             desc[2] = rg * R;
             desc[3] = min(R, rows - rg * R);
             desc[4] = slot;
-            desc[5] = c1 - cta;
+            desc[5] = (int)((end * grid + W - 1) / W) - cta;  // up to the first CTA that begins at `end` or behind
             desc[6] = sp.s.start;
         }
         __syncthreads();
@@ -528,53 +607,70 @@ __global__ void __launch_bounds__(kDecThreads, D == 64 ? 2 : 1) gdn_attn_decode_
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// Block (c, y) joins rows [y kJoinRows, (y + 1) kJoinRows) of the item that starts in CTA c and does not end there.
-constexpr int kJoinRows = 8, kJoinThreads = 256;
+// The blocks of a CTA's item (see JoinParams::blocks) take kJoinRows of its rows each.  An item in few parts gives a row
+// to every warp; one in many (a long context shared out among many CTAs) is summed by all warps a row at a time, warp w
+// taking parts w, w + 8, ... so that the loads of a row's parts are in flight together.
+constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinFew = 4;
+struct JoinKernel {
+    const int* desc;
+    const float* part;
+    const float* ml;
+    int grid, rows, blocks;  // CTAs of the attention kernel (0: not launched), its R, join blocks per CTA
+};
 struct JoinParams {
-    const int* desc[2];
-    const float* part[2];
-    const float* ml[2];
-    int grid[2];  // CTAs of each attention kernel (0: not launched)
-    int rows[2];  // R of each
+    JoinKernel k[2];
     void* o;
     float* lse;
     int G, hq, d, o_f32;
 };
 
-__global__ void __launch_bounds__(kJoinThreads) gdn_attn_join_kernel(const JoinParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const JoinParams p) {
+    __shared__ float4 s_a[kJoinWarps][32];
+    __shared__ float s_l[kJoinWarps];
     cudaGridDependencySynchronize();
-    int c = blockIdx.x, which = 0;
-    if (c >= p.grid[0]) c -= p.grid[0], which = 1;
-    const int* desc = p.desc[which] + (long long)c * kDescInts;
-    if (desc[0] < 0) return;
-    const int h = desc[1], row0 = desc[2], rows = desc[3], slot0 = desc[4], parts = desc[5], start = desc[6], R = p.rows[which];
-    const int tpr = p.d / 4, per = kJoinThreads / tpr;  // threads of a row, rows at a time
-    const int d4 = threadIdx.x % tpr;
-    for (int r = blockIdx.y * kJoinRows + threadIdx.x / tpr; r < min(rows, ((int)blockIdx.y + 1) * kJoinRows); r += per) {
-        const float* ml = p.ml[which];
+    const bool second = blockIdx.x >= p.k[0].grid * p.k[0].blocks;
+    const JoinKernel k = second ? p.k[1] : p.k[0];
+    const int b = blockIdx.x - (second ? p.k[0].grid * p.k[0].blocks : 0), c = b / k.blocks, y = b - c * k.blocks;
+    const int4 d0 = reinterpret_cast<const int4*>(k.desc)[c * 2], d1 = reinterpret_cast<const int4*>(k.desc)[c * 2 + 1];
+    if (d0.x < 0) return;
+    const int h = d0.y, row0 = d0.z, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool few = parts <= kJoinFew;
+    const bool mine = lane * 4 < p.d;
+    for (int r = y * kJoinRows + (few ? warp : 0); r < min(rows, (y + 1) * kJoinRows); r += few ? kJoinWarps : 1) {
+        auto at = [&](int i) { return ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r; };
         float mm = -INFINITY;
-        for (int i = 0; i < parts; ++i) mm = fmaxf(mm, ml[((((long long)(c + i) * 2 + (i ? 0 : slot0)) * R) + r) * 2]);
-        float ll = 0.f;
+        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, k.ml[at(i) * 2]);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = 0; i < parts; ++i) {
-            const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * R + r;
-            const float mi = ml[at * 2];
-            if (mi == -INFINITY && ml[at * 2 + 1] == 0.f) continue;  // nothing seen there: its sums are not written
-            const float f = mi == -INFINITY ? 1.f : exp2f(mi - mm);
-            const float4 b = reinterpret_cast<const float4*>(p.part[which] + at * p.d)[d4];
-            ll += ml[at * 2 + 1] * f;
-            a.x += b.x * f, a.y += b.y * f, a.z += b.z * f, a.w += b.w * f;
+        float ll = 0.f;
+#pragma unroll 4
+        for (int i = few ? 0 : warp; i < parts; i += few ? 1 : kJoinWarps) {
+            const float2 ml = *reinterpret_cast<const float2*>(k.ml + at(i) * 2);
+            const float4 v = mine ? *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+            if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen there: its sums may not have been written
+            const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mm);
+            ll += ml.y * f;
+            a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+        }
+        if (!few) {
+            __syncthreads();  // the last row's sums have been read
+            s_a[warp][lane] = a;
+            if (lane == 0) s_l[warp] = ll;
+            __syncthreads();
+            if (warp != 0) continue;
+#pragma unroll
+            for (int w = 1; w < kJoinWarps; ++w) {
+                const float4 v = s_a[w][lane];
+                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                ll += s_l[w];
+            }
         }
         const int row = row0 + r, tok = row / p.G, gh = row - tok * p.G;
-        const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
-        const float inv = ll == 0.f ? 0.f : 1.f / ll;
-        if (p.o_f32) {
-            reinterpret_cast<float4*>(static_cast<float*>(p.o) + at * p.d)[d4] = make_float4(a.x * inv, a.y * inv, a.z * inv, a.w * inv);
-        } else {
-            reinterpret_cast<uint2*>(static_cast<__nv_bfloat16*>(p.o) + at * p.d)[d4] =
-                make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
-        }
-        if (d4 == 0 && p.lse) p.lse[at] = ll == 0.f ? -INFINITY : (mm + log2f(ll)) * 0.6931471805599453f;
+        const long long out = (long long)(start + tok) * p.hq + h * p.G + gh;
+        if (mine) attn_store4(p.o, p.o_f32, out * p.d + 4 * lane, a, ll == 0.f ? 0.f : 1.f / ll);
+        if (lane == 0 && p.lse) p.lse[out] = attn_lse(mm, ll);
     }
 }
 

@@ -103,7 +103,8 @@ static void launch_read(const KvReadParams& p, bool e4m3, unsigned grid, unsigne
 // Which kernels a call launches, and its workspace: a function of the sizes that the host knows.  Sequences of up to
 // kDecMaxRows query rows per KV head belong to the decode kernel, longer ones to the chunk kernel.  Where every
 // sequence has as many tokens (no cu_seqlens) or there is but one, one kernel takes the call; a batch with no more
-// tokens than sequences is decoding, and the decode kernel takes all of it; else both run.
+// tokens than sequences is decoding, and the decode kernel takes all of it; else both run.  The decode kernel works on 8
+// rows at a time where that is enough (half the softmax and the accumulators), else on 16.
 constexpr int kDecMaxRows = 16;
 struct AttnArrays {
     int grid;  // 0: this kernel is not launched
@@ -111,10 +112,11 @@ struct AttnArrays {
 };
 struct AttnPlan {
     AttnArrays dec, tc;
-    int limit;  // the decode kernel's largest row count
+    int limit;     // the decode kernel's largest row count
+    int dec_rows;  // its rows at a time: 8 or 16
     size_t bytes;
 };
-static AttnPlan attn_plan(int n_tok, int n_seqs, bool packed, int G, int d) {
+static AttnPlan attn_plan(int n_tok, int n_seqs, bool packed, int G, int d, bool e4m3) {
     AttnPlan a = {};
     a.limit = 0x7fffffff;
     if (n_tok <= n_seqs) {
@@ -134,7 +136,9 @@ static AttnPlan attn_plan(int n_tok, int n_seqs, bool packed, int G, int d) {
         r.part = r.ml + (size_t)grid * 2 * rows * 2 * sizeof(float);
         a.bytes = r.part + (size_t)grid * 2 * rows * d * sizeof(float);
     };
-    place(a.dec, kAttnSms * (d == 64 ? 2 : 1), kDecRows);
+    a.dec_rows = (long long)G * (packed ? 1 : std::max(1, n_tok / n_seqs)) <= 8 ? 8 : 16;
+    const bool two = a.dec_rows == 8 && (e4m3 || d == 64);  // CTAs per SM, as DecTraits has it
+    place(a.dec, kAttnSms * (two ? 2 : 1), a.dec_rows);
     place(a.tc, kAttnSms, kTcRows);
     return a;
 }
@@ -145,6 +149,16 @@ static void use_arrays(AttnParams& p, const AttnArrays& r, uint8_t* ws) {
     p.part = reinterpret_cast<float*>(ws + r.part);
 }
 
+template <int D, bool E4M3, int R>
+static cudaError_t launch_decode(const AttnParams& p, int grid, unsigned* err, cudaStream_t stream) {
+    using Tr = DecTraits<D, E4M3, R>;
+    auto kern = gdn_attn_decode_kernel<D, E4M3, R>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tr::smem);
+    if (e != cudaSuccess) return e;
+    kern<<<grid, kDecThreads, Tr::smem, stream>>>(p, err);
+    return cudaGetLastError();
+}
+
 template <int D, bool E4M3>
 static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, JoinParams& j, unsigned* err, cudaStream_t stream) {
     cudaError_t e;
@@ -152,14 +166,10 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         use_arrays(p, plan.dec, ws);
         p.rows_lo = 0;
         p.rows_hi = plan.limit;
-        auto kern = gdn_attn_decode_kernel<D, E4M3>;
-        constexpr size_t smem = DecTraits<D, E4M3>::smem;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
-        kern<<<plan.dec.grid, kDecThreads, smem, stream>>>(p, err);
-        e = cudaGetLastError();
+        e = plan.dec_rows == 8 ? launch_decode<D, E4M3, 8>(p, plan.dec.grid, err, stream)
+                               : launch_decode<D, E4M3, 16>(p, plan.dec.grid, err, stream);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention decode kernel launch: %s", cudaGetErrorString(e));
-        j.desc[0] = p.desc, j.part[0] = p.part, j.ml[0] = p.ml, j.grid[0] = plan.dec.grid, j.rows[0] = kDecRows;
+        j.k[0] = {p.desc, p.part, p.ml, plan.dec.grid, plan.dec_rows, 1};
     }
     if (plan.tc.grid) {
         use_arrays(p, plan.tc, ws);
@@ -177,10 +187,10 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
-        j.desc[1] = p.desc, j.part[1] = p.part, j.ml[1] = p.ml, j.grid[1] = plan.tc.grid, j.rows[1] = kTcRows;
+        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, kTcRows / kJoinRows};
     }
-    const unsigned y = (plan.tc.grid ? kTcRows : kDecRows) / kJoinRows;
-    e = launch_after(gdn_attn_join_kernel, dim3(plan.dec.grid + plan.tc.grid, y), dim3(kJoinThreads), 0, stream, true, j);
+    const unsigned blocks = j.k[0].grid * j.k[0].blocks + j.k[1].grid * j.k[1].blocks;
+    e = launch_after(gdn_attn_join_kernel, dim3(blocks), dim3(kJoinWarps * 32), 0, stream, true, j);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;
 }
@@ -293,8 +303,9 @@ gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* 
 
 size_t gdn_paged_attn_workspace_bytes(int n_tok, int n_seqs, int Hq, int Hkv, int d) {
     if (n_tok < 1 || n_seqs < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || (d != 64 && d != 128)) return 0;
-    // a call with and one without cu_seqlens may differ: enough for either
-    return std::max(attn_plan(n_tok, n_seqs, true, Hq / Hkv, d).bytes, attn_plan(n_tok, n_seqs, false, Hq / Hkv, d).bytes);
+    size_t most = 0;  // enough for a call with or without cu_seqlens, over either cache
+    for (int i = 0; i < 4; ++i) most = std::max(most, attn_plan(n_tok, n_seqs, i & 1, Hq / Hkv, d, i & 2).bytes);
+    return most;
 }
 
 gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_cache, const void* v_cache,
@@ -319,7 +330,7 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     if ((st = check_stride("q_stride", q_stride, (long long)Hq * d, 2)) != GDN_OK) return st;
     if (!cu_seqlens && n_tok % n_seqs != 0)
         return fail(GDN_ERR_INVALID_ARG, "without cu_seqlens the tokens must divide evenly (%d over %d)", n_tok, n_seqs);
-    const AttnPlan plan = attn_plan(n_tok, n_seqs, cu_seqlens != nullptr, Hq / Hkv, d);
+    const AttnPlan plan = attn_plan(n_tok, n_seqs, cu_seqlens != nullptr, Hq / Hkv, d, cache_dt == GDN_E4M3);
     if (!workspace || ws_bytes < plan.bytes)
         return fail(GDN_ERR_INVALID_ARG, "the attention needs %zu bytes of workspace (got %zu)", plan.bytes, ws_bytes);
     unsigned* err = err_word_ptr(&st);

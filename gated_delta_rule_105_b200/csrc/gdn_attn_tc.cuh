@@ -575,7 +575,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             if (there) {
                 const float m2 = m == -INFINITY ? -INFINITY : m * cs;
                 if (whole) {
-                    if (p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m2 + log2f(l)) * 0.6931471805599453f;
+                    if (p.lse) p.lse[at] = attn_lse(m2, l);
                 } else {
                     p.ml[part * 2] = m2;
                     p.ml[part * 2 + 1] = l;
