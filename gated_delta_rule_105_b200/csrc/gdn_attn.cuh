@@ -138,10 +138,16 @@ __device__ __forceinline__ uint32_t e4m3_signed_to_bf16x2(uint32_t w) {
 __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, int hi) {
     return e4m3_signed_to_bf16x2(permute(w, 0, hi ? 0xb3a2 : 0x9180));
 }
-__device__ __forceinline__ void mma_e4m3(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
-                                         uint32_t b1) {
+// The same codes as an f16 pair: one conversion instruction, but f16's range is too short for weights times values.
+__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t w, int hi) {
+    uint32_t r;
+    asm("{.reg .b16 lo, up;\n\tmov.b32 {lo, up}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(r) : "r"(hi ? w >> 16 : w));
+    return r;
+}
+__device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
     asm volatile(
-        "mma.sync.aligned.m16n8k32.row.col.f32.e4m3.e4m3.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
@@ -158,7 +164,6 @@ template <int D, bool E4M3, int R> struct DecTraits {
     static constexpr int KL = D * (E4M3 ? 1 : 2) / 64;  // 16-byte K loads per thread and 8 keys
     static constexpr int MT = D / 16;                   // channel tiles of 16
     static constexpr int RS = R / 8;                    // sets of 8 rows
-    static constexpr int QF = E4M3 ? D / 32 : D / 16;   // k-steps
     static constexpr int CTAS = R == 8 && (E4M3 || D == 64) ? 2 : 1;  // per SM
     static constexpr size_t smem = kDecWarps * R * D * 4 + kDecWarps * R * 8 + 256;
 };
@@ -167,7 +172,7 @@ template <int D, bool E4M3, int R>
 __global__ void __launch_bounds__(kDecThreads, (DecTraits<D, E4M3, R>::CTAS))
 gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
     using Tr = DecTraits<D, E4M3, R>;
-    constexpr int KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS, QF = Tr::QF, NT = KS / 8, KG = KS / 16;
+    constexpr int KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS, NT = KS / 8, KG = KS / 16;
     extern __shared__ __align__(16) uint8_t smem[];
     float* s_o = reinterpret_cast<float*>(smem);                  // [warps][R][D]
     float* s_ml = s_o + kDecWarps * R * D;                        // [warps][R][2]
@@ -224,11 +229,9 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 
         // ---- the item's query rows: A fragments, in K's channel order
         const int row_lo = rg * R + g, rows = T * p.G;
-        // bf16 cache: a0, a2 of rows g and (R = 16) a1, a3 of rows g + 8.  8-bit cache: the row as q = 2^e (q1 + q2 / 16),
-        // two e4m3 rows with e per row: q1 takes 4 of bf16's 8 significant bits and q2 the exact rest, down to 2^-22 of
-        // the row's largest; so K's codes go into the matrix instruction as they are, without conversion, at twice
-        // bf16's rate.  R = 8: q1 in rows g and q2 in rows g + 8 of one fragment; R = 16: qf is q1 and qg is q2 of both.
-        uint32_t qf[QF][4], qg[E4M3 && R == 16 ? QF : 1][4];
+        // a0, a2 of rows g and (R = 16) a1, a3 of rows g + 8.  For the 8-bit cache Q becomes f16, each row divided by a
+        // power of two (exact down to 2^-28 of the row's largest), since K's codes convert to f16 in one instruction.
+        uint32_t qf[D / 16][4];
         float qscale[RS];
         int hi_[RS], lo_[RS];  // keys [lo_, hi_] that rows g and g + 8 see
 #pragma unroll
@@ -242,49 +245,31 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
             const __nv_bfloat16* q = p.q + (long long)(sp.s.start + tok) * p.q_stride + (h * p.G + gh) * D;
             qscale[r] = p.scale_log2;
             if (E4M3) {
-                // word s of a thread's 16 channels 64 j + 16 t is k-index 4t.. of half s & 1 of k-step 2 j + s / 2
-                uint2 u[D / 64][4];
                 unsigned top = 0;
 #pragma unroll
                 for (int j = 0; j < D / 64; ++j)
 #pragma unroll
                     for (int s = 0; s < 4; ++s) {
-                        u[j][s] = there ? *reinterpret_cast<const uint2*>(q + 64 * j + 16 * t + 4 * s) : make_uint2(0, 0);
-                        top = max(max(top, u[j][s].x & 0x7fffu), (u[j][s].x >> 16) & 0x7fffu);
-                        top = max(max(top, u[j][s].y & 0x7fffu), (u[j][s].y >> 16) & 0x7fffu);
+                        const uint2 u = there ? *reinterpret_cast<const uint2*>(q + 64 * j + 16 * t + 4 * s) : make_uint2(0, 0);
+                        qf[4 * j + s][r] = u.x;
+                        qf[4 * j + s][2 + r] = u.y;
+                        if (R == 8) qf[4 * j + s][1] = qf[4 * j + s][3] = 0;
+                        top = max(max(top, u.x & 0x7fffu), (u.x >> 16) & 0x7fffu);
+                        top = max(max(top, u.y & 0x7fffu), (u.y >> 16) & 0x7fffu);
                     }
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = max(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const bool bad = top >= 0x7f80u;  // an infinity or a NaN: the row's scores are NaN
-                int e = (int)(top >> 7) - 127 - 8 + ((top & 0x7fu) > 0x60u ? 1 : 0);
-                e = min(max(e, kScaleExpMin), kScaleExpMax);
+                // largest magnitude into [2^14, 2^15); an infinity or a NaN makes the row's scores NaN
+                const int e = min(max((int)(top >> 7) - 127 - 14, -100), 113);
                 const float inv = __int_as_float((127 - e) << 23);
-                qscale[r] = bad ? __int_as_float(0x7fc00000) : p.scale_log2 * __int_as_float((127 + e) << 23);
+                qscale[r] = top >= 0x7f80u ? __int_as_float(0x7fc00000) : p.scale_log2 * __int_as_float((127 + e) << 23);
 #pragma unroll
-                for (int j = 0; j < D / 64; ++j)
+                for (int i = 0; i < D / 16; ++i)
 #pragma unroll
-                    for (int s = 0; s < 4; ++s) {
-                        float x[4] = {__uint_as_float(u[j][s].x << 16), __uint_as_float(u[j][s].x & 0xffff0000u),
-                                      __uint_as_float(u[j][s].y << 16), __uint_as_float(u[j][s].y & 0xffff0000u)};
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) x[i] = bad ? 0.f : x[i] * inv;
-                        const uint32_t c1 = pack_e4m3x4(x[0], x[1], x[2], x[3]);
-                        float y[4];
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const __half2_raw h2 = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c1 >> (16 * i)), __NV_E4M3);
-                            const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&h2));
-                            y[2 * i] = f.x, y[2 * i + 1] = f.y;
-                        }
-                        const uint32_t c2 = pack_e4m3x4((x[0] - y[0]) * 16.f, (x[1] - y[1]) * 16.f, (x[2] - y[2]) * 16.f, (x[3] - y[3]) * 16.f);
-                        const int ks = 2 * j + (s >> 1), at = 2 * (s & 1);
-                        if (R == 8) {
-                            qf[ks][at] = c1;
-                            qf[ks][at + 1] = c2;
-                        } else {
-                            qf[ks][at + r] = c1;
-                            qg[ks][at + r] = c2;
-                        }
+                    for (int half = 0; half < 2; ++half) {
+                        const uint32_t u = qf[i][2 * half + r];
+                        const __half2 hq = __floats2half2_rn(__uint_as_float(u << 16) * inv, __uint_as_float(u & 0xffff0000u) * inv);
+                        qf[i][2 * half + r] = top >= 0x7f80u ? 0u : *reinterpret_cast<const uint32_t*>(&hq);
                     }
             } else {
 #pragma unroll
@@ -313,17 +298,22 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
         constexpr int ESZ = E4M3 ? 1 : 2;
 
         const int32_t* table = p.c.table + (long long)n * p.c.max_pages;
-        int prow[KG];  // row of the step's 16-key groups in the pool (below 2^31: checked on the host)
-        auto find = [&](int k0) {
+        // A step's pages are looked up two steps ahead, the entries used one step later: in between they are in flight.
+        int entry[KG], prow[KG];  // block-table entries; rows of the 16-key groups in the pool (below 2^31, see the host)
+        auto position = [&](int k0, int kg) { return min(k0 + 16 * kg, (len - 1) & ~15); };
+        auto look = [&](int k0) {
+#pragma unroll
+            for (int kg = 0; kg < KG; ++kg) entry[kg] = table[position(k0, kg) >> p.c.page_log2];
+        };
+        auto place = [&](int k0) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
-                const int kk = min(k0 + 16 * kg, (len - 1) & ~15);
-                int pg = table[kk >> p.c.page_log2];
+                int pg = entry[kg];
                 if ((unsigned)pg >= (unsigned)p.c.n_pages) {
                     if (lane == 0) atomicOr(err, kErrPages);
                     pg = 0;
                 }
-                prow[kg] = ((pg * p.c.hkv + h) << p.c.page_log2) + (kk & ((1 << p.c.page_log2) - 1));
+                prow[kg] = ((pg * p.c.hkv + h) << p.c.page_log2) + (position(k0, kg) & ((1 << p.c.page_log2) - 1));
             }
         };
         auto load_k = [&]() {
@@ -335,10 +325,10 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 if (E4M3) ksc[kt] = *reinterpret_cast<const uint16_t*>(p.c.k_scale + prow[kt >> 1] + 2 * t + 8 * (kt & 1));
             }
         };
-        auto load_v = [&](const int (&row)[KG]) {
+        auto load_v = [&]() {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
-                const uint8_t* at = static_cast<const uint8_t*>(p.c.v_cache) + (long long)(row[kg] + 2 * t) * (D * ESZ);
+                const uint8_t* at = static_cast<const uint8_t*>(p.c.v_cache) + (long long)(prow[kg] + 2 * t) * (D * ESZ);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     const uint8_t* base = at + ((i & 1) + 8 * (i >> 1)) * D * ESZ;
@@ -351,15 +341,16 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     if (!E4M3 && D == 128) vr2[kg][i] = *reinterpret_cast<const uint4*>(base + 128 + 16 * g);
                 }
                 if (E4M3) {
-                    vsc[2 * kg] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + row[kg] + 2 * t);
-                    vsc[2 * kg + 1] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + row[kg] + 8 + 2 * t);
+                    vsc[2 * kg] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 2 * t);
+                    vsc[2 * kg + 1] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 8 + 2 * t);
                 }
             }
         };
-        find(k_begin);
+        look(k_begin);
+        place(k_begin);
         load_k();
-        load_v(prow);
-        find(k_begin + UNIT);
+        load_v();
+        look(k_begin + UNIT);
 
         for (int x = 0; x < cnt; ++x) {
             const int k0 = k_begin + x * UNIT;
@@ -367,46 +358,33 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
             float s[NT][2 * RS];
 #pragma unroll
             for (int kt = 0; kt < NT; ++kt) {
-                float c[4] = {0.f, 0.f, 0.f, 0.f}, c2[4] = {0.f, 0.f, 0.f, 0.f};
+                float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < KL; ++j) {
                     const uint32_t kw[4] = {kr[kt][j].x, kr[kt][j].y, kr[kt][j].z, kr[kt][j].w};
+                    if (E4M3) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const uint32_t(&a)[4] = qf[2 * j + i];
-                        if (E4M3) {
-                            mma_e4m3(c, a[0], a[1], a[2], a[3], kw[2 * i], kw[2 * i + 1]);
-                            if (R == 16) {
-                                const uint32_t(&b)[4] = qg[(R == 16 && E4M3) ? 2 * j + i : 0];
-                                mma_e4m3(c2, b[0], b[1], b[2], b[3], kw[2 * i], kw[2 * i + 1]);
-                            }
-                        } else {
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t(&a)[4] = qf[4 * j + i];
+                            mma_f16(c, a[0], a[1], a[2], a[3], e4m3_pair_f16(kw[i], 0), e4m3_pair_f16(kw[i], 1));
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const uint32_t(&a)[4] = qf[2 * j + i];
                             mma_bf16(c, a[0], a[1], a[2], a[3], kw[2 * i], kw[2 * i + 1]);
                         }
                     }
                 }
-                if (E4M3) {
-                    const float k0s = kv_scale_value(ksc[kt] & 0xff), k1s = kv_scale_value(ksc[kt] >> 8);
-                    if (R == 8) {
-                        s[kt][0] = fmaf(c[2], 0.0625f, c[0]) * (qscale[0] * k0s);
-                        s[kt][1] = fmaf(c[3], 0.0625f, c[1]) * (qscale[0] * k1s);
-                    } else {
+                const float k0s = E4M3 ? kv_scale_value(ksc[kt] & 0xff) : 1.f, k1s = E4M3 ? kv_scale_value(ksc[kt] >> 8) : 1.f;
 #pragma unroll
-                        for (int i = 0; i < 2 * RS; ++i)
-                            s[kt][i] = fmaf(c2[i], 0.0625f, c[i]) * (qscale[i >> 1] * ((i & 1) ? k1s : k0s));
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * p.scale_log2;
-                }
+                for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * (E4M3 ? qscale[i >> 1] * ((i & 1) ? k1s : k0s) : p.scale_log2);
             }
             // ---- the next step's keys, and where the one after that lies
-            int vrow[KG];
-#pragma unroll
-            for (int kg = 0; kg < KG; ++kg) vrow[kg] = prow[kg];
             if (x + 1 < cnt) {
+                place(k0 + UNIT);
                 load_k();
-                find(k0 + 2 * UNIT);
+                look(k0 + 2 * UNIT);
             }
             // ---- mask: only steps that some row does not see whole
             const bool edge = k0 < full_lo || k0 + KS - 1 > full_hi;
@@ -524,7 +502,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     for (int r = 0; r < RS; ++r) mma_bf16(o[r][i], a0, a1, a2, a3, pf[2 * kg][r], pf[2 * kg + 1][r]);
                 }
             }
-            if (x + 1 < cnt) load_v(vrow);
+            if (x + 1 < cnt) load_v();
         }
 
         // ---- join the warps
@@ -607,15 +585,16 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// The blocks of a CTA's item (see JoinParams::blocks) take kJoinRows of its rows each.  An item in few parts gives a row
-// to every warp; one in many (a long context shared out among many CTAs) is summed by all warps a row at a time, warp w
-// taking parts w, w + 8, ... so that the loads of a row's parts are in flight together.
-constexpr int kJoinRows = 32, kJoinWarps = 8, kJoinFew = 4;
+// An item of the decode kernel has few rows and, of a long context, many parts: a block takes one row, warp w its parts w,
+// w + 8, ...  One of the chunk kernel has 256 rows and usually few parts: a warp takes a row, a block eight.  Eight parts'
+// loads are in flight at a time.
+constexpr int kJoinWarps = 8;
 struct JoinKernel {
     const int* desc;
     const float* part;
     const float* ml;
-    int grid, rows, blocks;  // CTAs of the attention kernel (0: not launched), its R, join blocks per CTA
+    int grid, rows, wpr;  // CTAs of the attention kernel (0: not launched), its R, warps per row (1 or 8)
+    __host__ __device__ int blocks() const { return rows * wpr / kJoinWarps; }  // per CTA
 };
 struct JoinParams {
     JoinKernel k[2];
@@ -628,16 +607,17 @@ __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const Jo
     __shared__ float4 s_a[kJoinWarps][32];
     __shared__ float s_l[kJoinWarps];
     cudaGridDependencySynchronize();
-    const bool second = blockIdx.x >= p.k[0].grid * p.k[0].blocks;
+    const int first = p.k[0].grid * p.k[0].blocks();
+    const bool second = (int)blockIdx.x >= first;
     const JoinKernel k = second ? p.k[1] : p.k[0];
-    const int b = blockIdx.x - (second ? p.k[0].grid * p.k[0].blocks : 0), c = b / k.blocks, y = b - c * k.blocks;
+    const int b = blockIdx.x - (second ? first : 0), c = b / k.blocks(), y = b - c * k.blocks();
     const int4 d0 = reinterpret_cast<const int4*>(k.desc)[c * 2], d1 = reinterpret_cast<const int4*>(k.desc)[c * 2 + 1];
     if (d0.x < 0) return;
     const int h = d0.y, row0 = d0.z, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool few = parts <= kJoinFew;
     const bool mine = lane * 4 < p.d;
-    for (int r = y * kJoinRows + (few ? warp : 0); r < min(rows, (y + 1) * kJoinRows); r += few ? kJoinWarps : 1) {
+    const int r = k.wpr == 1 ? y * kJoinWarps + warp : y;
+    if (r < rows) {  // one row a block, or one a warp
         auto at = [&](int i) { return ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r; };
         float mm = -INFINITY;
         for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, k.ml[at(i) * 2]);
@@ -645,25 +625,37 @@ __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const Jo
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
         float ll = 0.f;
-#pragma unroll 4
-        for (int i = few ? 0 : warp; i < parts; i += few ? 1 : kJoinWarps) {
-            const float2 ml = *reinterpret_cast<const float2*>(k.ml + at(i) * 2);
-            const float4 v = mine ? *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-            if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen there: its sums may not have been written
-            const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mm);
-            ll += ml.y * f;
-            a.x += v.x * f, a.y += v.y * f, a.z += v.z * f, a.w += v.w * f;
+        const int step = k.wpr;
+        for (int i0 = step == 1 ? 0 : warp; i0 < parts; i0 += 8 * step) {
+            float2 ml[8];
+            float4 v[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const int i = i0 + u * step;
+                ml[u] = make_float2(-INFINITY, 0.f);
+                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+                if (i < parts) {
+                    ml[u] = *reinterpret_cast<const float2*>(k.ml + at(i) * 2);
+                    if (mine) v[u] = *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane);
+                }
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;  // nothing seen there: its sums may not be written
+                const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - mm);
+                ll += ml[u].y * f;
+                a.x += v[u].x * f, a.y += v[u].y * f, a.z += v[u].z * f, a.w += v[u].w * f;
+            }
         }
-        if (!few) {
-            __syncthreads();  // the last row's sums have been read
+        if (step != 1) {
             s_a[warp][lane] = a;
             if (lane == 0) s_l[warp] = ll;
             __syncthreads();
-            if (warp != 0) continue;
+            if (warp != 0) return;
 #pragma unroll
             for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 v = s_a[w][lane];
-                a.x += v.x, a.y += v.y, a.z += v.z, a.w += v.w;
+                const float4 x = s_a[w][lane];
+                a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
                 ll += s_l[w];
             }
         }
