@@ -102,12 +102,20 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 
 // ------------------------------------------------------------------------------------------ few rows
 // mma.sync kernel for up to 16 query rows per item.  Bound by the cache's bytes: tensor work is small, and what counts
-// is that every warp keeps 16-byte loads in flight.  K and V go from global memory straight into the registers of
-// the matrix instructions, without shared memory: the order of the contraction index is free, so thread t of a quad
-// takes 8 (16 in 8 bits) consecutive channels of its key as its share of several k-steps (Q is loaded in the same
-// order), and for V the keys of a step are interleaved with byte permutes.
+// is that every warp keeps its loads in flight and spends few instructions per key.  Each warp has a ring of its own in
+// shared memory, filled with 16-byte asynchronous copies a few steps ahead, and no barrier with the other warps until the
+// item ends.  The order of the contraction index is free, so thread t of a quad takes 8 (16 in 8 bits) consecutive
+// channels of its key as its share of several k-steps (Q is loaded in the same order), and for V the keys of a step are
+// interleaved with byte permutes.  16-byte chunk c of row r lies at c ^ swizzle(r), which makes both reads free of bank
+// conflicts: K's (rows 2i and 2i + 1, chunks 0-3 or 4-7) and V's (rows 2t + const, chunks 2i and 2i + 1).
 //   S[q][key]: A = Q (16 rows), B = K; thread (g, t) = (lane / 4, lane % 4) gets rows g, g + 8 and keys 2t, 2t + 1.
 //   O^T[d][q]: A = V^T (16 channels x 16 keys), B = P^T, whose fragment is exactly S's: no shuffle in between.
+__device__ __forceinline__ uint32_t dec_swizzle(uint32_t r) { return ((((r >> 1) & 3u) ^ ((r & 1u) << 1)) << 1); }
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void copy_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                          uint32_t b1) {
     asm volatile(
@@ -155,27 +163,34 @@ __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
 
-constexpr int kDecThreads = 256, kDecWarps = 8;
 constexpr float kRescaleLog2 = 8.f;  // the running maximum follows only when it would be off by more than 2^8
 
 template <int D, bool E4M3, int R> struct DecTraits {
-    static constexpr int KS = D == 128 ? 16 : 32;       // keys of one warp step
-    static constexpr int UNIT = KS * kDecWarps;
-    static constexpr int KL = D * (E4M3 ? 1 : 2) / 64;  // 16-byte K loads per thread and 8 keys
-    static constexpr int MT = D / 16;                   // channel tiles of 16
-    static constexpr int RS = R / 8;                    // sets of 8 rows
-    static constexpr int CTAS = R == 8 && (E4M3 || D == 64) ? 2 : 1;  // per SM
-    static constexpr size_t smem = kDecWarps * R * D * 4 + kDecWarps * R * 8 + 256;
+    static constexpr int RB = D * (E4M3 ? 1 : 2);          // bytes of a row
+    static constexpr int WARPS = RB == 256 ? 8 : R == 8 ? 8 : 12;
+    static constexpr int CTAS = RB == 256 || R == 16 ? 1 : 2;  // per SM
+    static constexpr int THREADS = 32 * WARPS;
+    static constexpr int KS = RB == 64 ? 32 : 16;          // keys of one warp step
+    static constexpr int UNIT = KS * WARPS;
+    static constexpr int KL = RB / 64;                     // 16-byte K reads per thread and 8 keys
+    static constexpr int MT = D / 16;                      // channel tiles of 16
+    static constexpr int RS = R / 8;                       // sets of 8 rows
+    static constexpr int STAGE = 2 * KS * RB + (E4M3 ? 2 * KS : 0);
+    static constexpr int STAGES = 3;
+    static constexpr int RING = WARPS * STAGES * STAGE;
+    static constexpr int JOIN = WARPS * R * D * 4;         // in the ring's place once it is empty
+    static constexpr size_t smem = (RING > JOIN ? RING : JOIN) + WARPS * R * 8 + 256;
 };
 
 template <int D, bool E4M3, int R>
-__global__ void __launch_bounds__(kDecThreads, (DecTraits<D, E4M3, R>::CTAS))
+__global__ void __launch_bounds__((DecTraits<D, E4M3, R>::THREADS), (DecTraits<D, E4M3, R>::CTAS))
 gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
     using Tr = DecTraits<D, E4M3, R>;
-    constexpr int KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS, NT = KS / 8, KG = KS / 16;
-    extern __shared__ __align__(16) uint8_t smem[];
+    constexpr int kDecWarps = Tr::WARPS, kDecThreads = Tr::THREADS, KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS,
+                  RB = Tr::RB, STAGES = Tr::STAGES, NT = KS / 8, KG = KS / 16;
+    extern __shared__ __align__(128) uint8_t smem[];
     float* s_o = reinterpret_cast<float*>(smem);                  // [warps][R][D]
-    float* s_ml = s_o + kDecWarps * R * D;                        // [warps][R][2]
+    float* s_ml = reinterpret_cast<float*>(smem + (Tr::RING > Tr::JOIN ? Tr::RING : Tr::JOIN));  // [warps][R][2]
     long long* s_scan = reinterpret_cast<long long*>(s_ml + kDecWarps * R * 2);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, g = lane >> 2, t = lane & 3;
     const int cta = blockIdx.x, N = p.c.n_seq;
@@ -291,21 +306,20 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 #pragma unroll
         for (int r = 0; r < RS; ++r) m[r] = -INFINITY, l[r] = 0.f;
         const int k_begin = (sp.u_first + x0) * UNIT + warp * KS;
-        uint4 kr[NT][KL];
-        uint4 vr[KG][4];
-        uint4 vr2[!E4M3 && D == 128 ? KG : 1][4];  // channels 64.. of a bf16 row of 128
-        unsigned ksc[NT], vsc[NT];                 // scale bytes of keys 2t, 2t + 1 of each 8
-        constexpr int ESZ = E4M3 ? 1 : 2;
-
         const int32_t* table = p.c.table + (long long)n * p.c.max_pages;
-        // A step's pages are looked up two steps ahead, the entries used one step later: in between they are in flight.
-        int entry[KG], prow[KG];  // block-table entries; rows of the 16-key groups in the pool (below 2^31, see the host)
+        // This warp's ring.  A stage is KS rows of K, KS of V, and in 8 bits their scale bytes.
+        uint8_t* ring = smem + warp * STAGES * Tr::STAGE;
+        // Block-table entries are looked up one step before their rows are asked for.
+        int entry[KG];
         auto position = [&](int k0, int kg) { return min(k0 + 16 * kg, (len - 1) & ~15); };
         auto look = [&](int k0) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) entry[kg] = table[position(k0, kg) >> p.c.page_log2];
         };
-        auto place = [&](int k0) {
+        constexpr int CH = RB / 16, RPI = 32 / CH;  // chunks of a row, rows per copy instruction
+        const int c_row = lane / CH, c_ch = lane % CH;
+        auto fetch = [&](int k0, int stage) {
+            const uint32_t dst = sm100::smem_u32(ring + stage * Tr::STAGE);
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
                 int pg = entry[kg];
@@ -313,47 +327,57 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     if (lane == 0) atomicOr(err, kErrPages);
                     pg = 0;
                 }
-                prow[kg] = ((pg * p.c.hkv + h) << p.c.page_log2) + (position(k0, kg) & ((1 << p.c.page_log2) - 1));
-            }
-        };
-        auto load_k = [&]() {
+                // row of the 16 keys in the pool (below 2^31: checked on the host)
+                const int row = ((pg * p.c.hkv + h) << p.c.page_log2) + (position(k0, kg) & ((1 << p.c.page_log2) - 1));
+                const long long off = (long long)(row + c_row) * RB + c_ch * 16;
 #pragma unroll
-            for (int kt = 0; kt < NT; ++kt) {
-                const uint8_t* base = static_cast<const uint8_t*>(p.c.k_cache) + (long long)(prow[kt >> 1] + g) * (D * ESZ) + 16 * t + 8 * (kt & 1) * D * ESZ;
+                for (int kv = 0; kv < 2; ++kv) {
+                    const uint8_t* src = static_cast<const uint8_t*>(kv ? p.c.v_cache : p.c.k_cache) + off;
 #pragma unroll
-                for (int j = 0; j < KL; ++j) kr[kt][j] = *reinterpret_cast<const uint4*>(base + 64 * j);
-                if (E4M3) ksc[kt] = *reinterpret_cast<const uint16_t*>(p.c.k_scale + prow[kt >> 1] + 2 * t + 8 * (kt & 1));
-            }
-        };
-        auto load_v = [&]() {
-#pragma unroll
-            for (int kg = 0; kg < KG; ++kg) {
-                const uint8_t* at = static_cast<const uint8_t*>(p.c.v_cache) + (long long)(prow[kg] + 2 * t) * (D * ESZ);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const uint8_t* base = at + ((i & 1) + 8 * (i >> 1)) * D * ESZ;
-                    if (E4M3 && D == 64) {
-                        const uint2 u = *reinterpret_cast<const uint2*>(base + 8 * g);
-                        vr[kg][i] = make_uint4(u.x, u.y, 0, 0);
-                    } else {
-                        vr[kg][i] = *reinterpret_cast<const uint4*>(base + 16 * g);
+                    for (int i = 0; i < 16 / RPI; ++i) {
+                        const int r = c_row + i * RPI;
+                        const uint32_t ch = CH == 4 ? c_ch ^ ((r >> 1) & 3) : c_ch ^ dec_swizzle(r);
+                        copy16(dst + (kv * KS + kg * 16 + r) * RB + ch * 16, src + i * RPI * RB);
                     }
-                    if (!E4M3 && D == 128) vr2[kg][i] = *reinterpret_cast<const uint4*>(base + 128 + 16 * g);
                 }
-                if (E4M3) {
-                    vsc[2 * kg] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 2 * t);
-                    vsc[2 * kg + 1] = *reinterpret_cast<const uint16_t*>(p.c.v_scale + prow[kg] + 8 + 2 * t);
-                }
+                if (E4M3 && lane < 2)
+                    copy16(dst + 2 * KS * RB + lane * KS + kg * 16, (lane ? p.c.v_scale : p.c.k_scale) + row);
             }
+        };
+        // 16 bytes: chunk c of row r of K (kv 0) or V
+        auto read16 = [&](const uint8_t* st, int kv, int r, int c) {
+            const uint32_t ch = CH == 4 ? c ^ ((r >> 1) & 3) : c ^ dec_swizzle(r);
+            return *reinterpret_cast<const uint4*>(st + (kv * KS + r) * RB + ch * 16);
         };
         look(k_begin);
-        place(k_begin);
-        load_k();
-        load_v();
-        look(k_begin + UNIT);
+#pragma unroll
+        for (int i = 0; i < STAGES - 1; ++i) {
+            if (i < cnt) {
+                fetch(k_begin + i * UNIT, i);
+                look(k_begin + (i + 1) * UNIT);
+            }
+            copy_commit();
+        }
 
         for (int x = 0; x < cnt; ++x) {
             const int k0 = k_begin + x * UNIT;
+            const uint8_t* st = ring + (x % STAGES) * Tr::STAGE;
+            copy_wait<STAGES - 2>();
+            __syncwarp();
+            // every lane is done with the stage of the step before: it takes the rows of STAGES - 1 steps ahead
+            if (x + STAGES - 1 < cnt) {
+                fetch(k0 + (STAGES - 1) * UNIT, (x + STAGES - 1) % STAGES);
+                look(k0 + STAGES * UNIT);
+            }
+            copy_commit();
+            unsigned ksc[NT], vsc[NT];  // scale bytes of keys 2t, 2t + 1 of each 8
+            if (E4M3) {
+#pragma unroll
+                for (int kt = 0; kt < NT; ++kt) {
+                    ksc[kt] = *reinterpret_cast<const uint16_t*>(st + 2 * KS * RB + 8 * kt + 2 * t);
+                    vsc[kt] = *reinterpret_cast<const uint16_t*>(st + 2 * KS * RB + KS + 8 * kt + 2 * t);
+                }
+            }
             // ---- scores
             float s[NT][2 * RS];
 #pragma unroll
@@ -361,7 +385,8 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < KL; ++j) {
-                    const uint32_t kw[4] = {kr[kt][j].x, kr[kt][j].y, kr[kt][j].z, kr[kt][j].w};
+                    const uint4 kr = read16(st, 0, 8 * kt + g, 4 * j + t);
+                    const uint32_t kw[4] = {kr.x, kr.y, kr.z, kr.w};
                     if (E4M3) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
@@ -379,12 +404,6 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 const float k0s = E4M3 ? kv_scale_value(ksc[kt] & 0xff) : 1.f, k1s = E4M3 ? kv_scale_value(ksc[kt] >> 8) : 1.f;
 #pragma unroll
                 for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * (E4M3 ? qscale[i >> 1] * ((i & 1) ? k1s : k0s) : p.scale_log2);
-            }
-            // ---- the next step's keys, and where the one after that lies
-            if (x + 1 < cnt) {
-                place(k0 + UNIT);
-                load_k();
-                look(k0 + 2 * UNIT);
             }
             // ---- mask: only steps that some row does not see whole
             const bool edge = k0 < full_lo || k0 + KS - 1 > full_hi;
@@ -444,26 +463,35 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     pf[kt][r] = pack_bf16x2(a, b);
                 }
             }
-            // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values there are taken out, and
-            // the rows that do see such a key get a NaN weight instead (8-bit codes are always finite)
-            if (!E4M3 && edge) {
 #pragma unroll
-                for (int kg = 0; kg < KG; ++kg)
+            for (int kg = 0; kg < KG; ++kg) {
+                // V rows of keys 2t, 2t + 1, 2t + 8, 2t + 9: 16 bytes each (8 of a row of 64 codes; two of one of 256 bytes)
+                uint4 vr[4], vr2[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int r = 16 * kg + 2 * t + (i & 1) + 8 * (i >> 1);
+                    vr[i] = read16(st, 1, r, CH == 4 ? g >> 1 : g);
+                    if (CH == 4 && (g & 1)) vr[i].x = vr[i].z, vr[i].y = vr[i].w;
+                    if (CH == 16) vr2[i] = read16(st, 1, r, 8 + g);
+                }
+                // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values there are taken out, and
+                // the rows that do see such a key get a NaN weight instead (8-bit codes are always finite)
+                if (!E4M3 && edge) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        bool bad = bf16x2_nonfinite(vr[kg][i].x) || bf16x2_nonfinite(vr[kg][i].y) ||
-                                   bf16x2_nonfinite(vr[kg][i].z) || bf16x2_nonfinite(vr[kg][i].w);
-                        if (D == 128)
-                            bad = bad || bf16x2_nonfinite(vr2[kg][i].x) || bf16x2_nonfinite(vr2[kg][i].y) ||
-                                  bf16x2_nonfinite(vr2[kg][i].z) || bf16x2_nonfinite(vr2[kg][i].w);
+                        bool bad = bf16x2_nonfinite(vr[i].x) || bf16x2_nonfinite(vr[i].y) || bf16x2_nonfinite(vr[i].z) ||
+                                   bf16x2_nonfinite(vr[i].w);
+                        if (CH == 16)
+                            bad = bad || bf16x2_nonfinite(vr2[i].x) || bf16x2_nonfinite(vr2[i].y) ||
+                                  bf16x2_nonfinite(vr2[i].z) || bf16x2_nonfinite(vr2[i].w);
                         if (!__any_sync(0xffffffffu, bad)) continue;
                         unsigned any = bad;  // over the eight threads that hold this key
                         any |= __shfl_xor_sync(0xffffffffu, any, 4);
                         any |= __shfl_xor_sync(0xffffffffu, any, 8);
                         any |= __shfl_xor_sync(0xffffffffu, any, 16);
                         if (any) {
-                            vr[kg][i] = make_uint4(0, 0, 0, 0);
-                            if (D == 128) vr2[kg][i] = make_uint4(0, 0, 0, 0);
+                            vr[i] = make_uint4(0, 0, 0, 0);
+                            if (CH == 16) vr2[i] = make_uint4(0, 0, 0, 0);
                             const int kt = 2 * kg + (i >> 1), key = k0 + 8 * kt + 2 * t + (i & 1);
 #pragma unroll
                             for (int r = 0; r < RS; ++r)
@@ -471,10 +499,8 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                                     pf[kt][r] = (i & 1) ? (pf[kt][r] & 0xffffu) | 0x7fc00000u : (pf[kt][r] & 0xffff0000u) | 0x7fc0u;
                         }
                     }
-            }
-            // ---- O^T += V^T P^T
-#pragma unroll
-            for (int kg = 0; kg < KG; ++kg) {
+                }
+                // ---- O^T += V^T P^T
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     uint32_t a0, a1, a2, a3;
@@ -482,7 +508,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                         // channels 2i, 2i + 1 of this thread's 16 (8): codes of both keys of a pair, each with its sign
                         const int wd = i >> 1;
                         auto word = [&](const uint4& u) { return wd == 0 ? u.x : wd == 1 ? u.y : wd == 2 ? u.z : u.w; };
-                        const uint32_t x0 = word(vr[kg][0]), x1 = word(vr[kg][1]), x2 = word(vr[kg][2]), x3 = word(vr[kg][3]);
+                        const uint32_t x0 = word(vr[0]), x1 = word(vr[1]), x2 = word(vr[2]), x3 = word(vr[3]);
                         const unsigned sa = (i & 1) ? 0xe6a2 : 0xc480, sb = (i & 1) ? 0xf7b3 : 0xd591;
                         a0 = e4m3_signed_to_bf16x2(permute(x0, x1, sa));
                         a1 = e4m3_signed_to_bf16x2(permute(x0, x1, sb));
@@ -491,7 +517,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     } else {
                         const int wd = i & 3;
                         auto word = [&](const uint4& u) { return wd == 0 ? u.x : wd == 1 ? u.y : wd == 2 ? u.z : u.w; };
-                        const uint4(&vv)[4] = i < 4 ? vr[kg] : vr2[D == 128 ? kg : 0];
+                        const uint4(&vv)[4] = i < 4 ? vr : vr2;
                         const uint32_t x0 = word(vv[0]), x1 = word(vv[1]), x2 = word(vv[2]), x3 = word(vv[3]);
                         a0 = __byte_perm(x0, x1, 0x5410);
                         a1 = __byte_perm(x0, x1, 0x7632);
@@ -502,8 +528,8 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     for (int r = 0; r < RS; ++r) mma_bf16(o[r][i], a0, a1, a2, a3, pf[2 * kg][r], pf[2 * kg + 1][r]);
                 }
             }
-            if (x + 1 < cnt) load_v();
         }
+        __syncthreads();  // every warp's ring is read: the join takes its place
 
         // ---- join the warps
 #pragma unroll
@@ -585,16 +611,15 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// An item of the decode kernel has few rows and, of a long context, many parts: a block takes one row, warp w its parts w,
-// w + 8, ...  One of the chunk kernel has 256 rows and usually few parts: a warp takes a row, a block eight.  Eight parts'
-// loads are in flight at a time.
-constexpr int kJoinWarps = 8;
+// A warp takes a row; its lanes hold the parts' maxima and denominators, and the first parts' sums are asked for before
+// those have arrived.  An item of the decode kernel has few rows and may have many parts (one long context shared out
+// among all CTAs): then a block takes one row, warp w its parts w, w + 8, ...
+constexpr int kJoinWarps = 8, kJoinAhead = 4;
 struct JoinKernel {
     const int* desc;
     const float* part;
     const float* ml;
-    int grid, rows, wpr;  // CTAs of the attention kernel (0: not launched), its R, warps per row (1 or 8)
-    __host__ __device__ int blocks() const { return rows * wpr / kJoinWarps; }  // per CTA
+    int grid, rows, blocks;  // CTAs of the attention kernel (0: not launched), its R, join blocks per CTA
 };
 struct JoinParams {
     JoinKernel k[2];
@@ -603,51 +628,52 @@ struct JoinParams {
     int G, hq, d, o_f32;
 };
 
-__global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const JoinParams p) {
+__global__ void __launch_bounds__(kJoinWarps * 32, 4) gdn_attn_join_kernel(const JoinParams p) {
     __shared__ float4 s_a[kJoinWarps][32];
     __shared__ float s_l[kJoinWarps];
     cudaGridDependencySynchronize();
-    const int first = p.k[0].grid * p.k[0].blocks();
+    const int first = p.k[0].grid * p.k[0].blocks;
     const bool second = (int)blockIdx.x >= first;
-    const JoinKernel k = second ? p.k[1] : p.k[0];
-    const int b = blockIdx.x - (second ? first : 0), c = b / k.blocks(), y = b - c * k.blocks();
+    const JoinKernel k = {second ? p.k[1].desc : p.k[0].desc,   second ? p.k[1].part : p.k[0].part,
+                          second ? p.k[1].ml : p.k[0].ml,       second ? p.k[1].grid : p.k[0].grid,
+                          second ? p.k[1].rows : p.k[0].rows,   second ? p.k[1].blocks : p.k[0].blocks};
+    const int b = blockIdx.x - (second ? first : 0), c = b / k.blocks, y = b - c * k.blocks;
     const int4 d0 = reinterpret_cast<const int4*>(k.desc)[c * 2], d1 = reinterpret_cast<const int4*>(k.desc)[c * 2 + 1];
     if (d0.x < 0) return;
     const int h = d0.y, row0 = d0.z, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool mine = lane * 4 < p.d;
-    const int r = k.wpr == 1 ? y * kJoinWarps + warp : y;
-    if (r < rows) {  // one row a block, or one a warp
+    const bool shared_row = k.blocks == k.rows && parts > kJoinWarps;
+    const int r = shared_row ? y : y * kJoinWarps + warp, i_first = shared_row ? warp : 0, step = shared_row ? kJoinWarps : 1;
+    if (r < rows) {
+        const bool mine = lane * 4 < p.d;
         auto at = [&](int i) { return ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r; };
-        float mm = -INFINITY;
+        auto sums = [&](int i) {
+            return mine && i < parts ? *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 v[kJoinAhead];
+#pragma unroll
+        for (int u = 0; u < kJoinAhead; ++u) v[u] = sums(i_first + u * step);
+        float mm = -INFINITY, ll = 0.f;
         for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, k.ml[at(i) * 2]);
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        float ll = 0.f;
-        const int step = k.wpr;
-        for (int i0 = step == 1 ? 0 : warp; i0 < parts; i0 += 8 * step) {
-            float2 ml[8];
-            float4 v[8];
+        for (int i0 = i_first; i0 < parts; i0 += kJoinAhead * step) {
+            float2 ml[kJoinAhead];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const int i = i0 + u * step;
-                ml[u] = make_float2(-INFINITY, 0.f);
-                v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-                if (i < parts) {
-                    ml[u] = *reinterpret_cast<const float2*>(k.ml + at(i) * 2);
-                    if (mine) v[u] = *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane);
-                }
-            }
+            for (int u = 0; u < kJoinAhead; ++u)
+                ml[u] = i0 + u * step < parts ? *reinterpret_cast<const float2*>(k.ml + at(i0 + u * step) * 2) : make_float2(-INFINITY, 0.f);
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
+            for (int u = 0; u < kJoinAhead; ++u) {
+                const float4 x = v[u];
+                v[u] = sums(i0 + (u + kJoinAhead) * step);
                 if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;  // nothing seen there: its sums may not be written
                 const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - mm);
                 ll += ml[u].y * f;
-                a.x += v[u].x * f, a.y += v[u].y * f, a.z += v[u].z * f, a.w += v[u].w * f;
+                a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
             }
         }
-        if (step != 1) {
+        if (shared_row) {
             s_a[warp][lane] = a;
             if (lane == 0) s_l[warp] = ll;
             __syncthreads();

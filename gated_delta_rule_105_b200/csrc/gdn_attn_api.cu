@@ -155,7 +155,7 @@ static cudaError_t launch_decode(const AttnParams& p, int grid, unsigned* err, c
     auto kern = gdn_attn_decode_kernel<D, E4M3, R>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tr::smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, kDecThreads, Tr::smem, stream>>>(p, err);
+    kern<<<grid, Tr::THREADS, Tr::smem, stream>>>(p, err);
     return cudaGetLastError();
 }
 
@@ -169,7 +169,7 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         e = plan.dec_rows == 8 ? launch_decode<D, E4M3, 8>(p, plan.dec.grid, err, stream)
                                : launch_decode<D, E4M3, 16>(p, plan.dec.grid, err, stream);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention decode kernel launch: %s", cudaGetErrorString(e));
-        j.k[0] = {p.desc, p.part, p.ml, plan.dec.grid, plan.dec_rows, kJoinWarps};
+        j.k[0] = {p.desc, p.part, p.ml, plan.dec.grid, plan.dec_rows, plan.dec_rows};
     }
     if (plan.tc.grid) {
         use_arrays(p, plan.tc, ws);
@@ -187,9 +187,9 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
-        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, 1};
+        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, kTcRows / kJoinWarps};
     }
-    const unsigned blocks = j.k[0].grid * j.k[0].blocks() + j.k[1].grid * j.k[1].blocks();
+    const unsigned blocks = j.k[0].grid * j.k[0].blocks + j.k[1].grid * j.k[1].blocks;
     e = launch_after(gdn_attn_join_kernel, dim3(blocks), dim3(kJoinWarps * 32), 0, stream, true, j);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;
