@@ -110,7 +110,10 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 // conflicts: K's (rows 2i and 2i + 1, chunks 0-3 or 4-7) and V's (rows 2t + const, chunks 2i and 2i + 1).
 //   S[q][key]: A = Q (16 rows), B = K; thread (g, t) = (lane / 4, lane % 4) gets rows g, g + 8 and keys 2t, 2t + 1.
 //   O^T[d][q]: A = V^T (16 channels x 16 keys), B = P^T, whose fragment is exactly S's: no shuffle in between.
-__device__ __forceinline__ uint32_t dec_swizzle(uint32_t r) { return ((((r >> 1) & 3u) ^ ((r & 1u) << 1)) << 1); }
+template <int CH>  // chunks of a row; 4: two rows share the 128 bytes of all banks
+__host__ __device__ constexpr uint32_t dec_swizzle(uint32_t r) {
+    return CH == 4 ? (r >> 1) & 3u : ((((r >> 1) & 3u) ^ ((r & 1u) << 1)) << 1);
+}
 __device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
@@ -147,10 +150,10 @@ __device__ __forceinline__ uint32_t e4m3_pair(uint32_t w, int hi) {
     return e4m3_signed_to_bf16x2(permute(w, 0, hi ? 0xb3a2 : 0x9180));
 }
 // The same codes as an f16 pair: one conversion instruction, but f16's range is too short for weights times values.
-__device__ __forceinline__ uint32_t e4m3_pair_f16(uint32_t w, int hi) {
-    uint32_t r;
-    asm("{.reg .b16 lo, up;\n\tmov.b32 {lo, up}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;}" : "=r"(r) : "r"(hi ? w >> 16 : w));
-    return r;
+__device__ __forceinline__ void e4m3x4_f16(uint32_t w, uint32_t& lo, uint32_t& hi) {
+    asm("{.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(w));
 }
 __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
                                         uint32_t b1) {
@@ -159,6 +162,9 @@ __device__ __forceinline__ void mma_f16(float (&c)[4], uint32_t a0, uint32_t a1,
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The scales 2^(byte - 127) of the two bytes of `w`; infinity for the NaN scale.
+__device__ __forceinline__ float scale_lo(uint32_t w) { return __uint_as_float((w << 23) & 0x7f800000u); }
+__device__ __forceinline__ float scale_hi(uint32_t w) { return __uint_as_float((w << 15) & 0x7f800000u); }
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
@@ -175,7 +181,7 @@ template <int D, bool E4M3, int R> struct DecTraits {
     static constexpr int KL = RB / 64;                     // 16-byte K reads per thread and 8 keys
     static constexpr int MT = D / 16;                      // channel tiles of 16
     static constexpr int RS = R / 8;                       // sets of 8 rows
-    static constexpr int STAGE = 2 * KS * RB + (E4M3 ? 2 * KS : 0);
+    static constexpr int STAGE = 2 * KS * RB + (E4M3 ? 256 : 0);  // a multiple of 256: chunk numbers are XORed in place
     static constexpr int STAGES = 3;
     static constexpr int RING = WARPS * STAGES * STAGE;
     static constexpr int JOIN = WARPS * R * D * 4;         // in the ring's place once it is empty
@@ -188,7 +194,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
     using Tr = DecTraits<D, E4M3, R>;
     constexpr int kDecWarps = Tr::WARPS, kDecThreads = Tr::THREADS, KS = Tr::KS, UNIT = Tr::UNIT, KL = Tr::KL, MT = Tr::MT, RS = Tr::RS,
                   RB = Tr::RB, STAGES = Tr::STAGES, NT = KS / 8, KG = KS / 16;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(256) uint8_t smem[];
     float* s_o = reinterpret_cast<float*>(smem);                  // [warps][R][D]
     float* s_ml = reinterpret_cast<float*>(smem + (Tr::RING > Tr::JOIN ? Tr::RING : Tr::JOIN));  // [warps][R][2]
     long long* s_scan = reinterpret_cast<long long*>(s_ml + kDecWarps * R * 2);
@@ -308,7 +314,6 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
         const int k_begin = (sp.u_first + x0) * UNIT + warp * KS;
         const int32_t* table = p.c.table + (long long)n * p.c.max_pages;
         // This warp's ring.  A stage is KS rows of K, KS of V, and in 8 bits their scale bytes.
-        uint8_t* ring = smem + warp * STAGES * Tr::STAGE;
         // Block-table entries are looked up one step before their rows are asked for.
         int entry[KG];
         auto position = [&](int k0, int kg) { return min(k0 + 16 * kg, (len - 1) & ~15); };
@@ -316,10 +321,17 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) entry[kg] = table[position(k0, kg) >> p.c.page_log2];
         };
+        // Byte offsets in a stage.  Rows c_row + i RPI of a copy differ from row c_row in the swizzle by a constant per i;
+        // the rows of a K read do not differ at all, those of a V read by the key's parity.
         constexpr int CH = RB / 16, RPI = 32 / CH;  // chunks of a row, rows per copy instruction
         const int c_row = lane / CH, c_ch = lane % CH;
-        auto fetch = [&](int k0, int stage) {
-            const uint32_t dst = sm100::smem_u32(ring + stage * Tr::STAGE);
+        const uint32_t c_off = c_row * RB + ((c_ch ^ dec_swizzle<CH>(c_row)) << 4);
+        const uint32_t k_off = g * RB + ((t ^ dec_swizzle<CH>(g)) << 4);
+        const uint32_t v_off = KS * RB + 2 * t * RB + (((CH == 4 ? g >> 1 : g) ^ dec_swizzle<CH>(2 * t)) << 4);
+        const uint8_t* k_src = static_cast<const uint8_t*>(p.c.k_cache) + c_row * RB + c_ch * 16;
+        const uint8_t* v_src = static_cast<const uint8_t*>(p.c.v_cache) + c_row * RB + c_ch * 16;
+        const uint8_t* s_src = lane ? p.c.v_scale : p.c.k_scale;
+        auto fetch = [&](int k0, uint32_t dst) {
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
                 int pg = entry[kg];
@@ -329,31 +341,34 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 }
                 // row of the 16 keys in the pool (below 2^31: checked on the host)
                 const int row = ((pg * p.c.hkv + h) << p.c.page_log2) + (position(k0, kg) & ((1 << p.c.page_log2) - 1));
-                const long long off = (long long)(row + c_row) * RB + c_ch * 16;
+                const long long off = (long long)row * RB;
 #pragma unroll
-                for (int kv = 0; kv < 2; ++kv) {
-                    const uint8_t* src = static_cast<const uint8_t*>(kv ? p.c.v_cache : p.c.k_cache) + off;
-#pragma unroll
-                    for (int i = 0; i < 16 / RPI; ++i) {
-                        const int r = c_row + i * RPI;
-                        const uint32_t ch = CH == 4 ? c_ch ^ ((r >> 1) & 3) : c_ch ^ dec_swizzle(r);
-                        copy16(dst + (kv * KS + kg * 16 + r) * RB + ch * 16, src + i * RPI * RB);
-                    }
+                for (int i = 0; i < 16 / RPI; ++i) {
+                    const uint32_t to = (dst + c_off) ^ (dec_swizzle<CH>(i * RPI) << 4);
+                    copy16(to + (kg * 16 + i * RPI) * RB, k_src + off + i * RPI * RB);
+                    copy16(to + (KS + kg * 16 + i * RPI) * RB, v_src + off + i * RPI * RB);
                 }
-                if (E4M3 && lane < 2)
-                    copy16(dst + 2 * KS * RB + lane * KS + kg * 16, (lane ? p.c.v_scale : p.c.k_scale) + row);
+                if (E4M3 && lane < 2) copy16(dst + 2 * KS * RB + lane * KS + kg * 16, s_src + row);
             }
         };
-        // 16 bytes: chunk c of row r of K (kv 0) or V
-        auto read16 = [&](const uint8_t* st, int kv, int r, int c) {
-            const uint32_t ch = CH == 4 ? c ^ ((r >> 1) & 3) : c ^ dec_swizzle(r);
-            return *reinterpret_cast<const uint4*>(st + (kv * KS + r) * RB + ch * 16);
+        auto shared16 = [&](uint32_t at) {
+            uint4 u;
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(u.x), "=r"(u.y), "=r"(u.z), "=r"(u.w) : "r"(at) : "memory");
+            return u;
         };
+        auto shared_u16 = [&](uint32_t at) {
+            uint16_t u;
+            asm volatile("ld.shared.u16 %0, [%1];" : "=h"(u) : "r"(at) : "memory");
+            return (uint32_t)u;
+        };
+        const uint32_t ring = sm100::smem_u32(smem) + warp * STAGES * Tr::STAGE;
+        uint32_t st = ring, st_in = ring + (STAGES - 1) * Tr::STAGE;  // the stage in use and the one to fill
+        auto advance = [&](uint32_t& at) { at = at == ring + (STAGES - 1) * Tr::STAGE ? ring : at + Tr::STAGE; };
         look(k_begin);
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) {
             if (i < cnt) {
-                fetch(k_begin + i * UNIT, i);
+                fetch(k_begin + i * UNIT, ring + i * Tr::STAGE);
                 look(k_begin + (i + 1) * UNIT);
             }
             copy_commit();
@@ -361,12 +376,12 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 
         for (int x = 0; x < cnt; ++x) {
             const int k0 = k_begin + x * UNIT;
-            const uint8_t* st = ring + (x % STAGES) * Tr::STAGE;
             copy_wait<STAGES - 2>();
             __syncwarp();
             // every lane is done with the stage of the step before: it takes the rows of STAGES - 1 steps ahead
             if (x + STAGES - 1 < cnt) {
-                fetch(k0 + (STAGES - 1) * UNIT, (x + STAGES - 1) % STAGES);
+                fetch(k0 + (STAGES - 1) * UNIT, st_in);
+                advance(st_in);
                 look(k0 + STAGES * UNIT);
             }
             copy_commit();
@@ -374,8 +389,8 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
             if (E4M3) {
 #pragma unroll
                 for (int kt = 0; kt < NT; ++kt) {
-                    ksc[kt] = *reinterpret_cast<const uint16_t*>(st + 2 * KS * RB + 8 * kt + 2 * t);
-                    vsc[kt] = *reinterpret_cast<const uint16_t*>(st + 2 * KS * RB + KS + 8 * kt + 2 * t);
+                    ksc[kt] = shared_u16(st + 2 * t + 2 * KS * RB + 8 * kt);
+                    vsc[kt] = shared_u16(st + 2 * t + 2 * KS * RB + KS + 8 * kt);
                 }
             }
             // ---- scores
@@ -385,13 +400,15 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 float c[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                 for (int j = 0; j < KL; ++j) {
-                    const uint4 kr = read16(st, 0, 8 * kt + g, 4 * j + t);
+                    const uint4 kr = shared16(((st + k_off) ^ (64 * j)) + 8 * kt * RB);
                     const uint32_t kw[4] = {kr.x, kr.y, kr.z, kr.w};
                     if (E4M3) {
 #pragma unroll
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t(&a)[4] = qf[4 * j + i];
-                            mma_f16(c, a[0], a[1], a[2], a[3], e4m3_pair_f16(kw[i], 0), e4m3_pair_f16(kw[i], 1));
+                            uint32_t b0, b1;
+                            e4m3x4_f16(kw[i], b0, b1);
+                            mma_f16(c, a[0], a[1], a[2], a[3], b0, b1);
                         }
                     } else {
 #pragma unroll
@@ -401,9 +418,15 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                         }
                     }
                 }
-                const float k0s = E4M3 ? kv_scale_value(ksc[kt] & 0xff) : 1.f, k1s = E4M3 ? kv_scale_value(ksc[kt] >> 8) : 1.f;
+                if (E4M3) {
+                    const float ks[2] = {scale_lo(ksc[kt]), scale_hi(ksc[kt])};
+                    const float nan[2] = {ks[0] - ks[0], ks[1] - ks[1]};  // 0, or NaN for the NaN scale
 #pragma unroll
-                for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * (E4M3 ? qscale[i >> 1] * ((i & 1) ? k1s : k0s) : p.scale_log2);
+                    for (int i = 0; i < 2 * RS; ++i) s[kt][i] = fmaf(c[i] * qscale[i >> 1], ks[i & 1], nan[i & 1]);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 2 * RS; ++i) s[kt][i] = c[i] * p.scale_log2;
+                }
             }
             // ---- mask: only steps that some row does not see whole
             const bool edge = k0 < full_lo || k0 + KS - 1 > full_hi;
@@ -455,13 +478,21 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 for (int kt = 0; kt < NT; ++kt) {
                     float a = sm100::ex2_approx(s[kt][2 * r] - mu), b = sm100::ex2_approx(s[kt][2 * r + 1] - mu);
                     l[r] += a + b;
-                    if (E4M3) {
-                        // a key that this row does not see adds nothing, whatever its scale says
-                        a = edge && s[kt][2 * r] == -INFINITY ? 0.f : a * kv_scale_value(vsc[kt] & 0xff);
-                        b = edge && s[kt][2 * r + 1] == -INFINITY ? 0.f : b * kv_scale_value(vsc[kt] >> 8);
+                    if (E4M3) {  // (the NaN scale's codes are 0: infinity times them is NaN)
+                        a *= scale_lo(vsc[kt]);
+                        b *= scale_hi(vsc[kt]);
                     }
                     pf[kt][r] = pack_bf16x2(a, b);
                 }
+            }
+            if (E4M3 && edge) {  // a key that a row does not see adds nothing, whatever its scale says
+#pragma unroll
+                for (int kt = 0; kt < NT; ++kt)
+#pragma unroll
+                    for (int r = 0; r < RS; ++r) {
+                        if (s[kt][2 * r] == -INFINITY) pf[kt][r] &= 0xffff0000u;
+                        if (s[kt][2 * r + 1] == -INFINITY) pf[kt][r] &= 0xffffu;
+                    }
             }
 #pragma unroll
             for (int kg = 0; kg < KG; ++kg) {
@@ -469,10 +500,10 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 uint4 vr[4], vr2[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int r = 16 * kg + 2 * t + (i & 1) + 8 * (i >> 1);
-                    vr[i] = read16(st, 1, r, CH == 4 ? g >> 1 : g);
+                    const uint32_t at = ((st + v_off) ^ (dec_swizzle<CH>(i & 1) << 4)) + (16 * kg + (i & 1) + 8 * (i >> 1)) * RB;
+                    vr[i] = shared16(at);
                     if (CH == 4 && (g & 1)) vr[i].x = vr[i].z, vr[i].y = vr[i].w;
-                    if (CH == 16) vr2[i] = read16(st, 1, r, 8 + g);
+                    if (CH == 16) vr2[i] = shared16(at + 128);
                 }
                 // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values there are taken out, and
                 // the rows that do see such a key get a NaN weight instead (8-bit codes are always finite)
@@ -528,6 +559,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     for (int r = 0; r < RS; ++r) mma_bf16(o[r][i], a0, a1, a2, a3, pf[2 * kg][r], pf[2 * kg + 1][r]);
                 }
             }
+            advance(st);
         }
         __syncthreads();  // every warp's ring is read: the join takes its place
 
