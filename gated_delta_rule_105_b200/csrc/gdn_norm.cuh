@@ -28,30 +28,73 @@ struct NormParams {
     long long rows;
     int d;
     float eps;
+    int stages;  // of the ring
 };
 
-template <typename T> __device__ __forceinline__ void load8(const T* p, float (&x)[8]);
-template <> __device__ __forceinline__ void load8<__nv_bfloat16>(const __nv_bfloat16* p, float (&x)[8]) {
-    Vec16<__nv_bfloat16>::get(*reinterpret_cast<const uint4*>(p), x);
+// Largest magnitude of three, NaN if one is NaN.
+__device__ __forceinline__ float max_abs_nan(float a, float b, float c) {
+    float r;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
 }
-template <> __device__ __forceinline__ void load8<float>(const float* p, float (&x)[8]) {
-    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w, x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-template <typename T> __device__ __forceinline__ void store8(T* p, const float (&x)[8]);
-template <> __device__ __forceinline__ void store8<__nv_bfloat16>(__nv_bfloat16* p, const float (&x)[8]) {
-    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]), pack_bf16x2(x[4], x[5]),
-                                              pack_bf16x2(x[6], x[7]));
-}
-template <> __device__ __forceinline__ void store8<float>(float* p, const float (&x)[8]) {
-    reinterpret_cast<float4*>(p)[0] = make_float4(x[0], x[1], x[2], x[3]);
-    reinterpret_cast<float4*>(p)[1] = make_float4(x[4], x[5], x[6], x[7]);
-}
-
 __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+// Two fp32 operations per instruction: these kernels run out of issue slots before they run out of bandwidth otherwise.
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmul.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tadd.rn.f32x2 z, x, y;\n\tmov.b64 {%0, %1}, z;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{.reg .b64 x, y, z, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+// 8 channels as four pairs.
+struct F8 {
+    float2 v[4];
+};
+template <typename T> __device__ __forceinline__ F8 load_f8(const T* p);
+template <> __device__ __forceinline__ F8 load_f8<__nv_bfloat16>(const __nv_bfloat16* p) {
+    const uint4 u = *reinterpret_cast<const uint4*>(p);
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+    F8 r;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) r.v[i] = make_float2(__uint_as_float(w[i] << 16), __uint_as_float(w[i] & 0xffff0000u));
+    return r;
+}
+template <> __device__ __forceinline__ F8 load_f8<float>(const float* p) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    return F8{{make_float2(a.x, a.y), make_float2(a.z, a.w), make_float2(b.x, b.y), make_float2(b.z, b.w)}};
+}
+template <typename T> __device__ __forceinline__ void store_f8(T* p, const F8& x);
+template <> __device__ __forceinline__ void store_f8<__nv_bfloat16>(__nv_bfloat16* p, const F8& x) {
+    *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(x.v[0].x, x.v[0].y), pack_bf16x2(x.v[1].x, x.v[1].y),
+                                              pack_bf16x2(x.v[2].x, x.v[2].y), pack_bf16x2(x.v[3].x, x.v[3].y));
+}
+template <> __device__ __forceinline__ void store_f8<float>(float* p, const F8& x) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(x.v[0].x, x.v[0].y, x.v[1].x, x.v[1].y);
+    reinterpret_cast<float4*>(p)[1] = make_float4(x.v[2].x, x.v[2].y, x.v[3].x, x.v[3].y);
+}
+__device__ __forceinline__ void store_e4m3(uint8_t* p, const F8& x, float f) {
+    const float2 ff = make_float2(f, f);
+    const float2 a = mul2(x.v[0], ff), b = mul2(x.v[1], ff), c = mul2(x.v[2], ff), d = mul2(x.v[3], ff);
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack_e4m3x4(a.x, a.y, b.x, b.y), pack_e4m3x4(c.x, c.y, d.x, d.y));
 }
 
 // Reduction over the threads of a row: a warp's by shuffles; with several warps also through sm, in warp order, so
@@ -66,91 +109,152 @@ __device__ __forceinline__ float row_reduce(float v, int warps, float* sm) {
     if (warps == 1) return v;
     if ((threadIdx.x & 31) == 0) sm[threadIdx.x >> 5] = v;
     __syncthreads();
-    v = sm[0];
-    for (int w = 1; w < warps; ++w) v = MAX ? max_nan(v, sm[w]) : v + sm[w];
+    // up to 16 warps; what lies behind the last one's value is 0 (see the kernels' start)
+    const float4* q = reinterpret_cast<const float4*>(sm);
+    v = 0.f;
+    for (int w = 0; w < warps; w += 4) {
+        const float4 x = q[w >> 2];
+        v = MAX ? max_nan(max_abs_nan(x.x, x.y, x.z), max_nan(v, x.w)) : v + ((x.x + x.y) + (x.z + x.w));
+    }
     return v;
 }
+
+// Rows ahead of the one in work lie in shared memory: every thread copies the 8-channel units that it will use itself
+// (16-byte asynchronous copies), so no barrier stands between a copy and its use, and registers hold one row only.
+// Operand o of stage st is at [st][row of the block][o][unit].
+template <typename T, int OPS, int NV>
+struct NormRing {
+    uint8_t* base;      // this thread's first unit of stage 0, operand 0
+    int stages;         // 1 to 4
+    uint32_t op_bytes;  // one operand's row
+    uint32_t st_bytes;  // one stage of the block
+
+    __device__ __forceinline__ NormRing(uint8_t* smem, int d, int n) {
+        stages = n;
+        op_bytes = d * sizeof(T);
+        st_bytes = op_bytes * OPS * blockDim.y;
+        base = smem + threadIdx.y * (op_bytes * OPS) + threadIdx.x * 8 * sizeof(T);
+    }
+    __device__ __forceinline__ void fetch(int st, int o, const T* row, int units) const {
+        const uint32_t dst = sm100_smem(base + st * st_bytes + o * op_bytes);
+        const uint8_t* src = reinterpret_cast<const uint8_t*>(row + threadIdx.x * 8);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+            if ((int)threadIdx.x + i * (int)blockDim.x < units) {
+#pragma unroll
+                for (int k = 0; k < (int)sizeof(T) / 2; ++k) {
+                    const uint32_t off = i * blockDim.x * 8 * sizeof(T) + 16 * k;
+                    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + off), "l"(src + off) : "memory");
+                }
+            }
+    }
+    // Unit i of operand o.
+    __device__ __forceinline__ F8 get(int st, int o, int i) const {
+        return load_f8<T>(reinterpret_cast<const T*>(base + st * st_bytes + o * op_bytes) + i * blockDim.x * 8);
+    }
+    __device__ __forceinline__ void commit() const { asm volatile("cp.async.commit_group;" ::: "memory"); }
+    // All but the newest stages - 1 groups have landed.
+    __device__ __forceinline__ void wait() const {
+        if (stages == 4) asm volatile("cp.async.wait_group 3;" ::: "memory");
+        else if (stages == 3) asm volatile("cp.async.wait_group 2;" ::: "memory");
+        else if (stages == 2) asm volatile("cp.async.wait_group 1;" ::: "memory");
+        else asm volatile("cp.async.wait_group 0;" ::: "memory");
+    }
+    static __device__ __forceinline__ uint32_t sm100_smem(const void* p) {
+        return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+    }
+};
 
 enum NormOut : int { NORM_SAME = 0, NORM_ROW = 1, NORM_GROUP = 2 };
 constexpr int kNormGroup = 128;
 
-// blockDim = (threads of a row, rows of a block; more than one row only with one warp a row).  NV units of 8 channels
-// per thread.
+// blockDim = (threads of a row, rows at a time; more than one only with one warp a row).  NV units of 8 channels per
+// thread.  Block b takes rows b, b + gridDim.x, ... (times rows at a time).
 template <typename T, int NV, int OUT>
 __global__ void __launch_bounds__(512) gdn_add_rmsnorm_kernel(const NormParams p) {
-    __shared__ float sm[2][32];
-    const int tpr = blockDim.x, warps = tpr >> 5;
-    const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
-    if (row >= p.rows) return;  // whole warps; a block of several warps a row has one row
-    const int units = p.d >> 3;
-    const long long base = row * p.d;
-    float s[NV][8];
-    float sum = 0.f;
+    extern __shared__ __align__(16) uint8_t s_ring[];
+    __shared__ __align__(16) float sm[4][16];
+    const int tpr = blockDim.x, warps = tpr >> 5, units = p.d >> 3;
+    if (warps > 1) {
+        if (threadIdx.x < 64) (&sm[0][0])[threadIdx.x] = 0.f;
+        __syncthreads();
+    }
+    const float inv_d = 1.f / (float)p.d;
+    const NormRing<T, 2, NV> ring(s_ring, p.d, p.stages);
+    const long long first = (long long)blockIdx.x * blockDim.y + threadIdx.y, step = (long long)gridDim.x * blockDim.y;
+    auto ask = [&](long long row, int st) {
+        if (row < p.rows) {
+            ring.fetch(st, 0, static_cast<const T*>(p.x) + row * p.d, units);
+            if (p.res) ring.fetch(st, 1, static_cast<const T*>(p.res) + row * p.d, units);
+        }
+        ring.commit();
+    };
+    for (int i = 0; i < ring.stages - 1; ++i) ask(first + i * step, i);
+    F8 wt[NV] = {};  // a thread's channels are the same in every row
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int u = threadIdx.x + i * tpr;
-        if (u < units) {
-            load8<T>(static_cast<const T*>(p.x) + base + 8 * u, s[i]);
-            if (p.res) {
-                float r[8];
-                load8<T>(static_cast<const T*>(p.res) + base + 8 * u, r);
+    for (int i = 0; i < NV; ++i)
+        if ((int)threadIdx.x + i * tpr < units) wt[i] = load_f8<float>(p.weight + 8 * (threadIdx.x + i * tpr));
+    int st = 0, st_in = ring.stages - 1, buf = 0;
+    for (long long row = first; row < p.rows; row += step) {
+        ask(row + (ring.stages - 1) * step, st_in);
+        st_in = st_in + 1 == ring.stages ? 0 : st_in + 1;
+        ring.wait();
+        const long long base = row * p.d;
+        F8 s[NV];
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) s[i][e] += r[e];
+        for (int i = 0; i < NV; ++i) {
+            const int u = threadIdx.x + i * tpr;
+            if (u < units) {
+                s[i] = ring.get(st, 0, i);
+                if (p.res) {
+                    const F8 r = ring.get(st, 1, i);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) s[i].v[e] = add2(s[i].v[e], r.v[e]);
+                }
+                if (p.s) store_f8<T>(static_cast<T*>(p.s) + base + 8 * u, s[i]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum = fma2(s[i].v[e], s[i].v[e], sum);
             }
-        } else {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[i][e] = 0.f;
         }
-    }
+        st = st + 1 == ring.stages ? 0 : st + 1;
+        const float rstd = rsqrtf(fmaf(row_reduce<false>(sum.x + sum.y, warps, sm[buf]), inv_d, p.eps));
+        if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
+        const float2 rr = make_float2(rstd, rstd);
+        float amax = 0.f;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int u = threadIdx.x + i * tpr;
-        if (p.s && u < units) store8<T>(static_cast<T*>(p.s) + base + 8 * u, s[i]);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) sum += s[i][e] * s[i][e];
-    }
-    const float rstd = 1.f / sqrtf(row_reduce<false>(sum, warps, sm[0]) / (float)p.d + p.eps);
-    if (p.rstd && threadIdx.x == 0) p.rstd[row] = rstd;
-    float amax = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int u = threadIdx.x + i * tpr;
-        if (u < units) {
-            float w[8];
-            load8<float>(p.weight + 8 * u, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[i][e] = s[i][e] * rstd * w[e];
-            if (OUT == NORM_SAME) store8<T>(static_cast<T*>(p.y) + base + 8 * u, s[i]);
-        }
-        if (OUT != NORM_SAME) {
+        for (int i = 0; i < NV; ++i) {
+            const int u = threadIdx.x + i * tpr;
             if (OUT == NORM_GROUP) amax = 0.f;
+            if (u < units) {
 #pragma unroll
-            for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(s[i][e]));
+                for (int e = 0; e < 4; ++e) {
+                    s[i].v[e] = mul2(mul2(s[i].v[e], rr), wt[i].v[e]);
+                    if (OUT != NORM_SAME) amax = max_abs_nan(amax, s[i].v[e].x, s[i].v[e].y);
+                }
+                if (OUT == NORM_SAME) store_f8<T>(static_cast<T*>(p.y) + base + 8 * u, s[i]);
+            }
             if (OUT == NORM_GROUP) {
                 // 128 channels are 16 neighbouring threads of one unit (d is a multiple of 128)
 #pragma unroll
                 for (int o = 8; o > 0; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
                 if (u < units) {
-                    const float top = max_nan(amax, 1e-30f), inv = 448.f / top;
-                    *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + 8 * u) =
-                        make_uint2(pack_e4m3x4(s[i][0] * inv, s[i][1] * inv, s[i][2] * inv, s[i][3] * inv),
-                                   pack_e4m3x4(s[i][4] * inv, s[i][5] * inv, s[i][6] * inv, s[i][7] * inv));
-                    if ((u & 15) == 0) p.y_scale[row * (p.d / kNormGroup) + (u >> 4)] = top / 448.f;
+                    const float top = max_nan(amax, 1e-30f);
+                    store_e4m3(static_cast<uint8_t*>(p.y) + base + 8 * u, s[i], __fdividef(448.f, top));
+                    if ((u & 15) == 0) p.y_scale[row * (p.d / kNormGroup) + (u >> 4)] = top * (1.f / 448.f);
                 }
             }
         }
-    }
-    if (OUT == NORM_ROW) {
-        const float top = max_nan(row_reduce<true>(amax, warps, sm[1]), 1e-30f), inv = 448.f / top;
+        if (OUT == NORM_ROW) {
+            const float top = max_nan(row_reduce<true>(amax, warps, sm[2 + buf]), 1e-30f), inv = __fdividef(448.f, top);
 #pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int u = threadIdx.x + i * tpr;
-            if (u < units)
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(p.y) + base + 8 * u) =
-                    make_uint2(pack_e4m3x4(s[i][0] * inv, s[i][1] * inv, s[i][2] * inv, s[i][3] * inv),
-                               pack_e4m3x4(s[i][4] * inv, s[i][5] * inv, s[i][6] * inv, s[i][7] * inv));
+            for (int i = 0; i < NV; ++i) {
+                const int u = threadIdx.x + i * tpr;
+                if (u < units) store_e4m3(static_cast<uint8_t*>(p.y) + base + 8 * u, s[i], inv);
+            }
+            if (threadIdx.x == 0) p.y_scale[row] = top * (1.f / 448.f);
         }
-        if (threadIdx.x == 0) p.y_scale[row] = top / 448.f;
+        buf ^= 1;
     }
 }
 
@@ -166,82 +270,126 @@ struct NormBwdParams {
     float* dweight;  // [d]
     long long rows;
     int d, parts;
+    int stages;  // of the ring
 };
 
-// At most this many blocks' column sums: two per SM.
-constexpr int kNormBwdParts = 296;
-inline int norm_bwd_parts(long long rows) { return (int)(rows < kNormBwdParts ? rows : kNormBwdParts); }
-
-// Block b takes rows b, b + gridDim.x, ...; a thread owns the same channels in every row, so its dw stay in registers.
+// Block b takes rows b, b + gridDim.x, ...; a thread owns the same channels in every row, so its share of dw stays in
+// registers.  blockDim = (threads of a row, rows at a time): with one warp a row a block works on several, whose
+// dw are added through shared memory at the end.  A row's three operands are all asked for before the first is used.
 template <typename T, int NV>
 __global__ void __launch_bounds__(512) gdn_add_rmsnorm_bwd_kernel(const NormBwdParams p) {
-    __shared__ float sm[2][32];
+    extern __shared__ __align__(16) uint8_t s_ring[];
+    __shared__ __align__(16) float sm[2][16];
     const int tpr = blockDim.x, warps = tpr >> 5, units = p.d >> 3;
-    float dw[NV][8] = {};
-    int buf = 0;
-    for (long long row = blockIdx.x; row < p.rows; row += gridDim.x) {
+    if (warps > 1) {
+        if (threadIdx.x < 32) (&sm[0][0])[threadIdx.x] = 0.f;
+        __syncthreads();
+    }
+    const float inv_d = 1.f / (float)p.d;
+    cudaTriggerProgrammaticLaunchCompletion();  // the sum kernel may be brought up meanwhile
+    const NormRing<T, 3, NV> ring(s_ring, p.d, p.stages);
+    const long long first = (long long)blockIdx.x * blockDim.y + threadIdx.y, step = (long long)gridDim.x * blockDim.y;
+    auto ask = [&](long long row, int st) {
+        if (row < p.rows) {
+            ring.fetch(st, 0, static_cast<const T*>(p.s) + row * p.d, units);
+            ring.fetch(st, 1, static_cast<const T*>(p.dy) + row * p.d, units);
+            if (p.ds) ring.fetch(st, 2, static_cast<const T*>(p.ds) + row * p.d, units);
+        }
+        ring.commit();
+    };
+    for (int i = 0; i < ring.stages - 1; ++i) ask(first + i * step, i);
+    F8 dw[NV] = {}, wt[NV] = {};
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+        if ((int)threadIdx.x + i * tpr < units) wt[i] = load_f8<float>(p.weight + 8 * (threadIdx.x + i * tpr));
+    int st = 0, st_in = ring.stages - 1, buf = 0;
+    float rstd = first < p.rows ? p.rstd[first] : 0.f;
+    for (long long row = first; row < p.rows; row += step) {
+        ask(row + (ring.stages - 1) * step, st_in);
+        st_in = st_in + 1 == ring.stages ? 0 : st_in + 1;
+        const float rstd_next = row + step < p.rows ? p.rstd[row + step] : 0.f;
+        ring.wait();
         const long long base = row * p.d;
-        const float rstd = p.rstd[row];
-        float x[NV][8], gw[NV][8];
-        float sum = 0.f;
+        const float2 rr = make_float2(rstd, rstd);
+        float2 sum = make_float2(0.f, 0.f);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = threadIdx.x + i * tpr;
             if (u < units) {
-                load8<T>(static_cast<const T*>(p.s) + base + 8 * u, x[i]);
-                load8<T>(static_cast<const T*>(p.dy) + base + 8 * u, gw[i]);
-            } else {
+                const F8 x = ring.get(st, 0, i), y = ring.get(st, 1, i);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[i][e] = gw[i][e] = 0.f;
+                for (int e = 0; e < 4; ++e) {
+                    const float2 t = mul2(y.v[e], mul2(x.v[e], rr));
+                    dw[i].v[e] = add2(dw[i].v[e], t);
+                    sum = fma2(t, wt[i].v[e], sum);
+                }
             }
         }
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            const int u = threadIdx.x + i * tpr;
-            float w[8] = {};
-            if (u < units) load8<float>(p.weight + 8 * u, w);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                x[i][e] *= rstd;
-                dw[i][e] += gw[i][e] * x[i][e];
-                gw[i][e] *= w[e];
-                sum += gw[i][e] * x[i][e];
-            }
-        }
-        const float mean = row_reduce<false>(sum, warps, sm[buf]) / (float)p.d;
+        // dx = ds + rstd w dy - x (rstd^2 mean)
+        const float mean = row_reduce<false>(sum.x + sum.y, warps, sm[buf]) * inv_d, c = -rstd * rstd * mean;
+        const float2 cc = make_float2(c, c);
         buf ^= 1;
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int u = threadIdx.x + i * tpr;
             if (u < units) {
-                float r[8] = {};
-                if (p.ds) load8<T>(static_cast<const T*>(p.ds) + base + 8 * u, r);
+                const F8 x = ring.get(st, 0, i), y = ring.get(st, 1, i);
+                F8 r = {};
+                if (p.ds) r = ring.get(st, 2, i);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) r[e] += rstd * (gw[i][e] - x[i][e] * mean);
-                store8<T>(static_cast<T*>(p.dx) + base + 8 * u, r);
+                for (int e = 0; e < 4; ++e) r.v[e] = fma2(x.v[e], cc, fma2(mul2(y.v[e], wt[i].v[e]), rr, r.v[e]));
+                store_f8<T>(static_cast<T*>(p.dx) + base + 8 * u, r);
             }
         }
+        st = st + 1 == ring.stages ? 0 : st + 1;
+        rstd = rstd_next;
+    }
+    if (blockDim.y > 1) {
+        __syncthreads();  // the ring is read; the rows' dw of a block take its place, [rows at a time - 1][d]
+        float* s_dw = reinterpret_cast<float*>(s_ring);
+        if (threadIdx.y > 0) {
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int u = threadIdx.x + i * tpr;
+                if (u < units) store_f8<float>(s_dw + (threadIdx.y - 1) * p.d + 8 * u, dw[i]);
+            }
+        }
+        __syncthreads();
+        if (threadIdx.y > 0) return;
+        for (int y = 0; y < (int)blockDim.y - 1; ++y)
+#pragma unroll
+            for (int i = 0; i < NV; ++i) {
+                const int u = threadIdx.x + i * tpr;
+                if (u < units) {
+                    const F8 o = load_f8<float>(s_dw + y * p.d + 8 * u);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) dw[i].v[e] = add2(dw[i].v[e], o.v[e]);
+                }
+            }
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
         const int u = threadIdx.x + i * tpr;
-        if (u < units) store8<float>(p.part + (long long)blockIdx.x * p.d + 8 * u, dw[i]);
+        if (u < units) store_f8<float>(p.part + (long long)blockIdx.x * p.d + 8 * u, dw[i]);
     }
 }
 
-// Column sums of the blocks' sums, in a fixed order: 32 channels per block, 8 warps that take every eighth row.
-__global__ void __launch_bounds__(256) gdn_add_rmsnorm_dw_kernel(const NormBwdParams p) {
-    __shared__ float sm[8][33];
+// Column sums of the blocks' sums, in a fixed order: 32 channels per block, warp w takes rows w, w + 32, ...
+constexpr int kDwWarps = 32;
+__global__ void __launch_bounds__(kDwWarps * 32) gdn_add_rmsnorm_dw_kernel(const NormBwdParams p) {
+    __shared__ float sm[kDwWarps][33];
     cudaGridDependencySynchronize();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, c = blockIdx.x * 32 + lane;
     float v = 0.f;
-    if (c < p.d)
-        for (int i = warp; i < p.parts; i += 8) v += p.part[(long long)i * p.d + c];
+    if (c < p.d) {
+#pragma unroll 4
+        for (int i = warp; i < p.parts; i += kDwWarps) v += p.part[(long long)i * p.d + c];
+    }
     sm[warp][lane] = v;
     __syncthreads();
     if (warp == 0 && c < p.d) {
 #pragma unroll
-        for (int w = 1; w < 8; ++w) v += sm[w][lane];
+        for (int w = 1; w < kDwWarps; ++w) v += sm[w][lane];
         p.dweight[c] = v;
     }
 }
