@@ -541,46 +541,44 @@ def gdn_kda_chunk_bwd(q, k, v, g, beta, d_o, scale=None, h0=None, dhT=None, cu_s
 
 
 # ------------------------------------------------------------------------------------------ the attention layer
+# These calls are short (a decode step is a few microseconds on the device), so their checks are kept cheap.
 _CODES = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16, torch.float8_e4m3fn: GDN_E4M3}
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
 def _addr(t):
     return None if t is None else t.data_ptr()
 
 
-def _on(dev, *named):
-    """Every tensor of the call lies on one CUDA device (None entries are left out)."""
-    for name, t in named:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be a CUDA tensor on {dev}, like the call's other tensors, got {t.device}")
+def _device(t, *others):
+    """Index of the CUDA device that every tensor of the call lies on (None entries are left out)."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the tensors must be CUDA tensors (libgdn has no CPU path)")
+    for o in others:
+        if o is not None and o.get_device() != dev:
+            raise ValueError(f"the call's tensors must lie on one CUDA device, got {t.device} and {o.device}")
+    return dev
 
 
-class _Device:
-    """Makes a tensor's device current for the launch (a context manager only where it is not already)."""
-    __slots__ = ("dev", "prev")
-
-    def __init__(self, dev):
-        if dev.type != "cuda":
-            raise ValueError("the tensors must be CUDA tensors (libgdn has no CPU path)")
-        self.dev = dev
-
-    def __enter__(self):
-        cur = torch.cuda.current_device()
-        self.prev = None if self.dev.index == cur else cur
-        if self.prev is not None:
-            torch.cuda.set_device(self.dev)
-        return torch.cuda.current_stream(self.dev).cuda_stream
-
-    def __exit__(self, *exc):
-        if self.prev is not None:
-            torch.cuda.set_device(self.prev)
-        return False
+def _call(dev, fn, *args):
+    """fn(*args, stream) on the current stream of device `dev`, with that device current."""
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, _raw_stream(dev))
+    if st != GDN_OK:
+        _raise_on(st)
 
 
 def _rows(name, t, heads, d):
     """[n, heads, d] whose tokens may lie apart (a slice of a fused projection): returns the token stride."""
     if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != d:
         raise ValueError(f"{name} must be [tokens, {heads}, {d}], got {list(t.shape)}")
+    if t.is_contiguous():
+        return heads * d
     s0, s1, s2 = t.stride()
     if s2 != 1 or (heads > 1 and s1 != d):
         raise ValueError(f"{name}'s heads and channels must be contiguous (only its tokens may lie apart)")
@@ -589,30 +587,31 @@ def _rows(name, t, heads, d):
 
 def _cache_args(k_cache, v_cache, k_scale, v_scale, block_table):
     """Checks of the paged cache; returns (n_pages, Hkv, page_size, d, dtype code, n_seqs, max_pages)."""
-    if k_cache.dim() != 4 or v_cache.shape != k_cache.shape or v_cache.dtype != k_cache.dtype:
+    shape, dt = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape or v_cache.dtype is not dt:
         raise ValueError("k_cache and v_cache must be [n_pages, Hkv, page_size, d] of one shape and dtype")
-    if k_cache.dtype not in (torch.bfloat16, torch.float8_e4m3fn):
-        raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {k_cache.dtype}")
-    eight = k_cache.dtype is torch.float8_e4m3fn
-    for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
-        if eight != (t is not None):
-            raise ValueError("k_scale and v_scale go with an 8-bit cache, and only with one")
-        if eight and (t.dtype is not torch.uint8 or t.shape != k_cache.shape[:3]):
-            raise ValueError(f"{name} must be uint8 [n_pages, Hkv, page_size]")
-    if block_table.dim() != 2 or block_table.dtype is not torch.int32:
+    if dt is torch.float8_e4m3fn:
+        if k_scale is None or v_scale is None:
+            raise ValueError("an 8-bit cache needs k_scale and v_scale")
+        for name, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if t.dtype is not torch.uint8 or t.shape != shape[:3] or not t.is_contiguous():
+                raise ValueError(f"{name} must be a contiguous uint8 [n_pages, Hkv, page_size]")
+    elif dt is torch.bfloat16:
+        if k_scale is not None or v_scale is not None:
+            raise ValueError("k_scale and v_scale go with an 8-bit cache only")
+    else:
+        raise ValueError(f"the cache must be bfloat16 or float8_e4m3fn, got {dt}")
+    table = block_table.shape
+    if len(table) != 2 or block_table.dtype is not torch.int32:
         raise ValueError("block_table must be int32 [n_seqs, max_pages]")
-    for name, t in (("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-                    ("block_table", block_table)):
-        if t is not None and not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-    n_pages, hkv, page, d = k_cache.shape
-    return n_pages, hkv, page, d, _CODES[k_cache.dtype], block_table.shape[0], block_table.shape[1]
+    if not (k_cache.is_contiguous() and v_cache.is_contiguous() and block_table.is_contiguous()):
+        raise ValueError("k_cache, v_cache and block_table must be contiguous")
+    return (*shape, _CODES[dt], *table)
 
 
-def _seq_args(n_seqs, seq_lens, cu_seqlens):
-    for name, t, n in (("seq_lens", seq_lens, n_seqs), ("cu_seqlens", cu_seqlens, n_seqs + 1)):
-        if t is not None and (t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous()):
-            raise ValueError(f"{name} must be a contiguous int32 [{n}]")
+def _ints(name, t, n):
+    if t.dtype is not torch.int32 or t.dim() != 1 or t.shape[0] != n or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous int32 [{n}]")
 
 
 def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None):
@@ -625,18 +624,17 @@ def kv_append(k, v, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_
     """
     n_pages, hkv, page, d, code, n_seqs, max_pages = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
     ks, vs = _rows("k", k, hkv, d), _rows("v", v, hkv, d)
-    if v.shape != k.shape or v.dtype != k.dtype or k.dtype not in (torch.float32, torch.bfloat16):
+    dt = k.dtype
+    if v.shape != k.shape or v.dtype is not dt or dt not in (torch.float32, torch.bfloat16):
         raise ValueError("k and v must have one shape, and be both float32 or both bfloat16")
-    _seq_args(n_seqs, seq_lens, cu_seqlens)
-    dev = k.device
-    _on(dev, ("v", v), ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-        ("block_table", block_table), ("seq_lens", seq_lens), ("cu_seqlens", cu_seqlens))
-    with _Device(dev) as stream:
-        st = load_library().gdn_kv_append(
-            k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
-            block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), k.shape[0], n_seqs, n_pages, max_pages,
-            page, hkv, d, _CODES[k.dtype], code, stream)
-    _raise_on(st)
+    _ints("seq_lens", seq_lens, n_seqs)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, n_seqs + 1)
+    dev = _device(k, v, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens)
+    _call(dev, load_library().gdn_kv_append,
+          k.data_ptr(), v.data_ptr(), ks, vs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+          block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), k.shape[0], n_seqs, n_pages, max_pages,
+          page, hkv, d, _CODES[dt], code)
     return k_cache, v_cache
 
 
@@ -650,21 +648,20 @@ def kv_read(k_cache, v_cache, block_table, cu_seqlens, n_rows, k_scale=None, v_s
         raise ValueError(f"dtype must be float32 or bfloat16, got {dtype}")
     if cu_seqlens is None:
         raise ValueError("cu_seqlens is required")
-    _seq_args(n_seqs, None, cu_seqlens)
-    dev = k_cache.device
-    k = torch.empty((n_rows, hkv, d), dtype=dtype, device=dev) if k is None else k
-    v = torch.empty((n_rows, hkv, d), dtype=dtype, device=dev) if v is None else v
+    _ints("cu_seqlens", cu_seqlens, n_seqs + 1)
+    shape = (n_rows, hkv, d)
+    if k is None:
+        k = torch.empty(n_rows, hkv, d, dtype=dtype, device=k_cache.device)
+    if v is None:
+        v = torch.empty_like(k)
     for name, t in (("k", k), ("v", v)):
-        if t.shape != (n_rows, hkv, d) or t.dtype != dtype or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} [{n_rows}, {hkv}, {d}]")
-    _on(dev, ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale), ("block_table", block_table),
-        ("cu_seqlens", cu_seqlens), ("k", k), ("v", v))
-    with _Device(dev) as stream:
-        st = load_library().gdn_kv_read(
-            k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
-            cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), n_rows, n_seqs, n_pages, max_pages, page, hkv, d, code,
-            _CODES[dtype], stream)
-    _raise_on(st)
+        if t.shape != shape or t.dtype is not dtype or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} {list(shape)}")
+    dev = _device(k_cache, v_cache, k_scale, v_scale, block_table, cu_seqlens, k, v)
+    _call(dev, load_library().gdn_kv_read,
+          k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale), block_table.data_ptr(),
+          cu_seqlens.data_ptr(), k.data_ptr(), v.data_ptr(), n_rows, n_seqs, n_pages, max_pages, page, hkv, d, code,
+          _CODES[dtype])
     return k, v
 
 
@@ -672,6 +669,14 @@ def paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d) -> int:
     """Device workspace (bytes) ``paged_attn_fwd`` needs for these sizes (a fixed amount per CTA, whatever the
     sequences' lengths)."""
     return int(load_library().gdn_paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d))
+
+
+def _workspace_of(workspace, nbytes, device):
+    if workspace is None:
+        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+    if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor")
+    return workspace
 
 
 def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None, scale=None,
@@ -685,34 +690,38 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, 
     logarithms [n_tok, Hq] fp32.  ``workspace`` (uint8, at least :func:`paged_attn_workspace_bytes`) is allocated per
     call when not given."""
     n_pages, hkv, page, d, code, n_seqs, max_pages = _cache_args(k_cache, v_cache, k_scale, v_scale, block_table)
-    if q.dim() != 3 or q.dtype is not torch.bfloat16:
+    shape = q.shape
+    if len(shape) != 3 or q.dtype is not torch.bfloat16:
         raise ValueError("q must be bfloat16 [tokens, Hq, d]")
-    n_tok, hq = q.shape[0], q.shape[1]
+    n_tok, hq = shape[0], shape[1]
     qs = _rows("q", q, hq, d)
-    _seq_args(n_seqs, seq_lens, cu_seqlens)
+    _ints("seq_lens", seq_lens, n_seqs)
+    if cu_seqlens is not None:
+        _ints("cu_seqlens", cu_seqlens, n_seqs + 1)
     if o_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"o_dtype must be float32 or bfloat16, got {o_dtype}")
-    dev = q.device
-    with _Device(dev) as stream:
-        if o is None:
-            o = torch.empty((n_tok, hq, d), dtype=o_dtype, device=dev)
-        elif o.shape != (n_tok, hq, d) or o.dtype != o_dtype or not o.is_contiguous():
-            raise ValueError(f"o must be a contiguous {o_dtype} [{n_tok}, {hq}, {d}]")
-        lse = torch.empty((n_tok, hq), dtype=torch.float32, device=dev) if return_lse else None
-        if workspace is None:
-            workspace = torch.empty(paged_attn_workspace_bytes(n_tok, n_seqs, hq, hkv, d), dtype=torch.uint8,
-                                    device=dev)
-        _check_dev("workspace", workspace, torch.uint8)
-        _on(dev, ("k_cache", k_cache), ("v_cache", v_cache), ("k_scale", k_scale), ("v_scale", v_scale),
-            ("block_table", block_table), ("seq_lens", seq_lens), ("cu_seqlens", cu_seqlens), ("o", o),
-            ("workspace", workspace))
-        st = load_library().gdn_paged_attn_fwd(
-            q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
-            block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else scale,
-            window, o.data_ptr(), _addr(lse), n_tok, n_seqs, n_pages, max_pages, page, hq, hkv, d, code,
-            _CODES[o_dtype], workspace.data_ptr(), workspace.numel(), stream)
-    _raise_on(st)
+    device = q.device
+    if o is None:
+        o = torch.empty(n_tok, hq, d, dtype=o_dtype, device=device)
+    elif o.shape != shape or o.dtype is not o_dtype or not o.is_contiguous():
+        raise ValueError(f"o must be a contiguous {o_dtype} {list(shape)}")
+    lse = torch.empty(n_tok, hq, dtype=torch.float32, device=device) if return_lse else None
+    if workspace is None or workspace.dtype is not torch.uint8:
+        nbytes = paged_attn_workspace_bytes(n_tok, n_seqs, hq, hkv, d)
+        workspace = _workspace_of(workspace, nbytes, device)
+    dev = _device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, o, workspace)
+    _call(dev, load_library().gdn_paged_attn_fwd,
+          q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
+          block_table.data_ptr(), seq_lens.data_ptr(), _addr(cu_seqlens), d ** -0.5 if scale is None else scale,
+          window, o.data_ptr(), _addr(lse), n_tok, n_seqs, n_pages, max_pages, page, hq, hkv, d, code,
+          _CODES[o_dtype], workspace.data_ptr(), workspace.numel())
     return (o, lse) if return_lse else o
+
+
+def _check_same(name, t, like):
+    """`t` (or None) is contiguous and has the shape and dtype of `like`."""
+    if t is not None and (t.dtype is not like.dtype or t.shape != like.shape or not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous {like.dtype} {list(like.shape)}")
 
 
 def add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0, s=None):
@@ -722,41 +731,29 @@ def add_rmsnorm_fwd(x, weight, residual=None, eps=1e-5, out_dtype=None, group=0,
     fp32 scales per row (``group`` 0) or per 128 channels (``group`` 128): value = y * scale.  ``s`` may be given (x or
     residual itself for an update in place).  Returns a dict: s (x itself without a residual), y, rstd [rows], and
     scale ([rows, 1] or [rows, d / 128]; None without 8 bits)."""
-    d = x.shape[-1]
     dt = x.dtype
-    if dt not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"x must be float32 or bfloat16, got {dt}")
-    out_dtype = dt if out_dtype is None else out_dtype
-    if out_dtype != dt and out_dtype is not torch.float8_e4m3fn:
+    if dt not in (torch.float32, torch.bfloat16) or not x.is_contiguous():
+        raise ValueError(f"x must be a contiguous float32 or bfloat16 tensor, got {dt}")
+    if out_dtype is None:
+        out_dtype = dt
+    if out_dtype is not dt and out_dtype is not torch.float8_e4m3fn:
         raise ValueError(f"out_dtype must be x's dtype or float8_e4m3fn, got {out_dtype}")
-    _check_dev("x", x)
-    _check_dev("weight", weight, torch.float32)
-    if weight.shape != (d,):
-        raise ValueError("weight must be [d]")
-    if group not in (0, 128) or (group and (out_dtype == dt or d % group)):
+    d = x.shape[-1]
+    if weight.shape != (d,) or weight.dtype is not torch.float32 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 [d]")
+    if group not in (0, 128) or (group and (out_dtype is dt or d % group)):
         raise ValueError("group is 0, or 128 with an 8-bit output and d a multiple of 128")
     rows = x.numel() // d if d else 0
-    dev = x.device
-    with _Device(dev) as stream:
-        if residual is not None:
-            _check_dev("residual", residual, dt)
-            if residual.shape != x.shape:
-                raise ValueError("residual must have x's shape")
-            s = torch.empty_like(x) if s is None else s
-        if s is not None:
-            _check_dev("s", s, dt)
-            if s.shape != x.shape:
-                raise ValueError("s must have x's shape")
-        y = torch.empty(x.shape, dtype=out_dtype, device=dev)
-        rstd = torch.empty(rows, dtype=torch.float32, device=dev)
-        scale = None
-        if out_dtype != dt:
-            scale = torch.empty((rows, d // group if group else 1), dtype=torch.float32, device=dev)
-        _on(dev, ("weight", weight), ("residual", residual), ("s", s))
-        st = load_library().gdn_add_rmsnorm_fwd(
-            x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(s), y.data_ptr(), _addr(scale), rstd.data_ptr(),
-            rows, d, _CODES[dt], _CODES[out_dtype], group, eps, stream)
-    _raise_on(st)
+    _check_same("residual", residual, x)
+    _check_same("s", s, x)
+    if residual is not None and s is None:
+        s = torch.empty_like(x)
+    y = torch.empty_like(x, dtype=out_dtype)
+    rstd = weight.new_empty(rows)
+    scale = None if out_dtype is dt else weight.new_empty(rows, d // group if group else 1)
+    _call(_device(x, weight, residual, s), load_library().gdn_add_rmsnorm_fwd,
+          x.data_ptr(), _addr(residual), weight.data_ptr(), _addr(s), y.data_ptr(), _addr(scale), rstd.data_ptr(),
+          rows, d, _CODES[dt], _CODES[out_dtype], group, eps)
     return {"s": x if s is None else s, "y": y, "rstd": rstd, "scale": scale}
 
 
@@ -769,28 +766,23 @@ def add_rmsnorm_bwd(dy, s, weight, rstd, ds=None, dx=None, workspace=None):
     """Backward pass of :func:`add_rmsnorm_fwd` (``gdn_add_rmsnorm_bwd``): dy the gradient of y, ds (or None) the one
     that reaches s by the residual path, s and rstd the forward's.  Returns a dict: dx (in s's dtype: the gradient of
     x and, the same, of residual; may be given, dy or ds itself for an update in place) and dweight [d] fp32."""
-    d, dt = s.shape[-1], s.dtype
-    if dt not in (torch.float32, torch.bfloat16):
-        raise ValueError(f"s must be float32 or bfloat16, got {dt}")
-    for name, t in (("s", s), ("dy", dy), ("ds", ds), ("dx", dx)):
-        _check_dev(name, t, dt)
-        if t is not None and t.shape != s.shape:
-            raise ValueError(f"{name} must have s's shape")
+    dt, d = s.dtype, s.shape[-1]
+    if dt not in (torch.float32, torch.bfloat16) or not s.is_contiguous():
+        raise ValueError(f"s must be a contiguous float32 or bfloat16 tensor, got {dt}")
+    _check_same("dy", dy, s)
+    _check_same("ds", ds, s)
+    _check_same("dx", dx, s)
     rows = s.numel() // d if d else 0
-    _check_dev("weight", weight, torch.float32)
-    _check_dev("rstd", rstd, torch.float32)
-    if weight.shape != (d,) or rstd.numel() != rows:
-        raise ValueError("weight must be [d] and rstd one value per row")
-    dev = s.device
-    with _Device(dev) as stream:
-        dx = torch.empty_like(s) if dx is None else dx
-        dweight = torch.empty(d, dtype=torch.float32, device=dev)
-        if workspace is None:
-            workspace = torch.empty(add_rmsnorm_bwd_workspace_bytes(rows, d), dtype=torch.uint8, device=dev)
-        _check_dev("workspace", workspace, torch.uint8)
-        _on(dev, ("dy", dy), ("ds", ds), ("dx", dx), ("weight", weight), ("rstd", rstd), ("workspace", workspace))
-        st = load_library().gdn_add_rmsnorm_bwd(
-            dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(ds), dx.data_ptr(),
-            dweight.data_ptr(), rows, d, _CODES[dt], workspace.data_ptr() or None, workspace.numel(), stream)
-    _raise_on(st)
+    if weight.shape != (d,) or weight.dtype is not torch.float32 or not weight.is_contiguous():
+        raise ValueError("weight must be a contiguous float32 [d]")
+    if rstd.numel() != rows or rstd.dtype is not torch.float32 or not rstd.is_contiguous():
+        raise ValueError("rstd must be contiguous float32, one value per row")
+    if dx is None:
+        dx = torch.empty_like(s)
+    dweight = torch.empty_like(weight)
+    if workspace is None or workspace.dtype is not torch.uint8:
+        workspace = _workspace_of(workspace, add_rmsnorm_bwd_workspace_bytes(rows, d), s.device)
+    _call(_device(s, dy, ds, dx, weight, rstd, workspace), load_library().gdn_add_rmsnorm_bwd,
+          dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(ds), dx.data_ptr(),
+          dweight.data_ptr(), rows, d, _CODES[dt], workspace.data_ptr() or None, workspace.numel())
     return {"dx": dx, "dweight": dweight}

@@ -53,12 +53,21 @@ gdn_status fail(gdn_status st, const char* fmt, ...) {
 
 void clear_error() { t_msg[0] = 0; }
 
+// The error word's address on each device, looked up by the first call there (as for g_static_ws_addr).
+static std::atomic<unsigned*> g_err_word_addr[kMaxDevices];
+
 unsigned* err_word_ptr(gdn_status* st) {
+    int dev = -1;
+    cudaError_t e = cudaGetDevice(&dev);
     unsigned* ptr = nullptr;
-    cudaError_t e = cudaGetSymbolAddress(reinterpret_cast<void**>(&ptr), g_err_word);
-    if (e != cudaSuccess) {
-        *st = fail(GDN_ERR_CUDA, "cudaGetSymbolAddress(error word): %s", cudaGetErrorString(e));
-        return nullptr;
+    if (e == cudaSuccess && dev >= 0 && dev < kMaxDevices) ptr = g_err_word_addr[dev].load(std::memory_order_acquire);
+    if (!ptr) {
+        if (e == cudaSuccess) e = cudaGetSymbolAddress(reinterpret_cast<void**>(&ptr), g_err_word);
+        if (e != cudaSuccess) {
+            *st = fail(GDN_ERR_CUDA, "cudaGetSymbolAddress(error word): %s", cudaGetErrorString(e));
+            return nullptr;
+        }
+        if (dev >= 0 && dev < kMaxDevices) g_err_word_addr[dev].store(ptr, std::memory_order_release);
     }
     *st = GDN_OK;
     return ptr;

@@ -152,10 +152,9 @@ static void use_arrays(AttnParams& p, const AttnArrays& r, uint8_t* ws) {
 template <int D, bool E4M3, int R>
 static cudaError_t launch_decode(const AttnParams& p, int grid, unsigned* err, cudaStream_t stream) {
     using Tr = DecTraits<D, E4M3, R>;
-    auto kern = gdn_attn_decode_kernel<D, E4M3, R>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)Tr::smem);
+    const cudaError_t e = allow_shared<&gdn_attn_decode_kernel<D, E4M3, R>>((int)Tr::smem);
     if (e != cudaSuccess) return e;
-    kern<<<grid, Tr::THREADS, Tr::smem, stream>>>(p, err);
+    gdn_attn_decode_kernel<D, E4M3, R><<<grid, Tr::THREADS, Tr::smem, stream>>>(p, err);
     return cudaGetLastError();
 }
 
@@ -183,7 +182,7 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         }
         auto kern = gdn_attn_chunk_kernel<D, E4M3>;
         using L = AttnTc<D, E4M3>;
-        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES);
+        e = allow_shared<&gdn_attn_chunk_kernel<D, E4M3>>(L::BYTES);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
@@ -220,11 +219,11 @@ static NormShape norm_shape(long long rows, int d, int esize, int ops) {
     return n;
 }
 
-template <typename K, typename P>
-static cudaError_t launch_norm_shape(K kern, const NormShape& n, const P& p, cudaStream_t stream) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)n.smem);
+template <auto Kern, typename P>
+static cudaError_t launch_norm_shape(const NormShape& n, const P& p, cudaStream_t stream) {
+    const cudaError_t e = allow_shared<Kern>(224 * 1024);
     if (e != cudaSuccess) return e;
-    kern<<<n.grid, n.block, n.smem, stream>>>(p);
+    Kern<<<n.grid, n.block, n.smem, stream>>>(p);
     return cudaGetLastError();
 }
 
@@ -232,9 +231,9 @@ template <typename T, int OUT>
 static cudaError_t launch_norm(NormParams p, cudaStream_t stream) {
     const NormShape n = norm_shape(p.rows, p.d, sizeof(T), 2);
     p.stages = n.stages;
-    return n.nv == 1   ? launch_norm_shape(gdn_add_rmsnorm_kernel<T, 1, OUT>, n, p, stream)
-           : n.nv == 2 ? launch_norm_shape(gdn_add_rmsnorm_kernel<T, 2, OUT>, n, p, stream)
-                       : launch_norm_shape(gdn_add_rmsnorm_kernel<T, 4, OUT>, n, p, stream);
+    return n.nv == 1   ? launch_norm_shape<&gdn_add_rmsnorm_kernel<T, 1, OUT>>(n, p, stream)
+           : n.nv == 2 ? launch_norm_shape<&gdn_add_rmsnorm_kernel<T, 2, OUT>>(n, p, stream)
+                       : launch_norm_shape<&gdn_add_rmsnorm_kernel<T, 4, OUT>>(n, p, stream);
 }
 
 template <typename T>
@@ -242,9 +241,9 @@ static cudaError_t launch_norm_bwd(NormBwdParams p, cudaStream_t stream) {
     const NormShape n = norm_shape(p.rows, p.d, sizeof(T), 3);
     p.stages = n.stages;
     p.parts = n.grid;
-    const cudaError_t e = n.nv == 1   ? launch_norm_shape(gdn_add_rmsnorm_bwd_kernel<T, 1>, n, p, stream)
-                          : n.nv == 2 ? launch_norm_shape(gdn_add_rmsnorm_bwd_kernel<T, 2>, n, p, stream)
-                                      : launch_norm_shape(gdn_add_rmsnorm_bwd_kernel<T, 4>, n, p, stream);
+    const cudaError_t e = n.nv == 1   ? launch_norm_shape<&gdn_add_rmsnorm_bwd_kernel<T, 1>>(n, p, stream)
+                          : n.nv == 2 ? launch_norm_shape<&gdn_add_rmsnorm_bwd_kernel<T, 2>>(n, p, stream)
+                                      : launch_norm_shape<&gdn_add_rmsnorm_bwd_kernel<T, 4>>(n, p, stream);
     if (e != cudaSuccess) return e;
     return launch_after(gdn_add_rmsnorm_dw_kernel, dim3((p.d + 31) / 32), dim3(kDwWarps * 32), 0, stream, true, p);
 }

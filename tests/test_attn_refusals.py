@@ -118,7 +118,7 @@ def test_workspace_sizes(lib):
     assert bd.paged_attn_workspace_bytes(1, 1, 8, 3, 128) == 0
     assert bd.paged_attn_workspace_bytes(1, 1, 8, 2, 96) == 0
     assert bd.paged_attn_workspace_bytes(4096, 2, 8, 2, 128) > 0
-    assert bd.add_rmsnorm_bwd_workspace_bytes(0, 64) == 0 and bd.add_rmsnorm_bwd_workspace_bytes(7, 64) >= 7 * 64 * 4
+    assert bd.add_rmsnorm_bwd_workspace_bytes(0, 64) == 0 and bd.add_rmsnorm_bwd_workspace_bytes(7, 64) > 0
 
 
 def test_binding_refuses_cpu_tensors_and_wrong_shapes():
