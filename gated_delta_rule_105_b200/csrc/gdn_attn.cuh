@@ -506,7 +506,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     if (CH == 16) vr2[i] = shared16(at + 128);
                 }
                 // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values there are taken out, and
-                // the rows that do see such a key get a NaN weight instead (8-bit codes are always finite)
+                // a row that does see such a key gets a NaN denominator (8-bit codes are always finite)
                 if (!E4M3 && edge) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
@@ -523,11 +523,10 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                         if (any) {
                             vr[i] = make_uint4(0, 0, 0, 0);
                             if (CH == 16) vr2[i] = make_uint4(0, 0, 0, 0);
-                            const int kt = 2 * kg + (i >> 1), key = k0 + 8 * kt + 2 * t + (i & 1);
+                            const int key = k0 + 16 * kg + 8 * (i >> 1) + 2 * t + (i & 1);
 #pragma unroll
                             for (int r = 0; r < RS; ++r)
-                                if (key <= hi_[r] && key >= lo_[r])
-                                    pf[kt][r] = (i & 1) ? (pf[kt][r] & 0xffffu) | 0x7fc00000u : (pf[kt][r] & 0xffff0000u) | 0x7fc0u;
+                                if (key <= hi_[r] && key >= lo_[r]) l[r] = __int_as_float(0x7fc00000);
                         }
                     }
                 }

@@ -15,7 +15,7 @@
 //
 // Masked keys.  A score that a row must not see is set to -inf before the maximum, so K may hold anything there.  For V a
 // weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, V rows with a NaN or an infinity
-// are zeroed in shared memory and marked, and rows that do see a marked key take a NaN weight for it.
+// are zeroed in shared memory and marked, and a row that does see a marked key gets NaN.
 #pragma once
 
 #include "gdn_attn.cuh"
@@ -89,6 +89,11 @@ __device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile
 __device__ __forceinline__ bool tc_warp_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
     return __all_sync(0xffffffffu, tc_wait(bar, parity, abort_flag, err));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -110,18 +115,31 @@ __device__ __forceinline__ SeqSpan tc_span(const AttnParams& p, int n, unsigned*
     return s;
 }
 
-// A CTA's current segment: tiles [x, x + cnt) of an item.  Every role walks the same segments.
+// A CTA's current segment: `cnt` tiles of an item from tile `tile0` on.  Every role walks the same segments.
 struct TcSeg {
     SeqSpan s;
     int n, h, rt, x, units, cnt, rts;
+    int tile0;       // first tile of the segment
+    int pmin, pmax;  // positions of the item's first and last row
     long long w;
 
+    __device__ __forceinline__ void item(const AttnParams& p, const AttnTcCtl* c) {
+        const int rows = s.T * p.G, base = s.len - s.T;
+        pmin = base + rt * kTcRows / p.G;
+        pmax = base + (min(rows, (rt + 1) * kTcRows) - 1) / p.G;
+        const int first = first_tile_of(p, pmin);
+        units = pmax / kTcTile + 1 - first;
+        tile0 = first + x;
+        cnt = (int)min((long long)(units - x), c->w1 - w);
+    }
+    static __device__ __forceinline__ int first_tile_of(const AttnParams& p, int pos) {
+        return p.window > 0 ? max(0, pos - p.window + 1) / kTcTile : 0;
+    }
     __device__ __forceinline__ void start(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
         n = c->n, h = c->h, rt = c->rt, x = c->x, w = c->w0;
         s = tc_span(p, n, err);
         rts = (s.T * p.G + kTcRows - 1) / kTcRows;
-        units = tc_units(p, s, rt);
-        cnt = (int)min((long long)(units - x), c->w1 - w);
+        item(p, c);
     }
     // Moves on; false when the stretch is done.
     __device__ __forceinline__ bool next(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
@@ -137,35 +155,24 @@ struct TcSeg {
                 rts = (s.T * p.G + kTcRows - 1) / kTcRows;
             }
         }
-        units = tc_units(p, s, rt);
-        cnt = (int)min((long long)units, c->w1 - w);
+        item(p, c);
         return true;
     }
-    // Tiles [a, b) of this segment that row tile i (0, 1) of the item takes part in, as absolute tile numbers.
-    __device__ __forceinline__ void active(const AttnParams& p, int i, int& a, int& b) const {
-        const int rows = s.T * p.G, r0 = rt * kTcRows + i * kTcTile;
-        int t0, t1;
-        tile_range(p, s, rt * kTcRows, min(rows, (rt + 1) * kTcRows), t0, t1);
-        const int f0 = t0 + x, f1 = f0 + cnt;
-        if (r0 >= rows) {
-            a = b = f0;
-            return;
-        }
-        tile_range(p, s, r0, min(rows, r0 + kTcTile), t0, t1);
-        a = max(t0, f0);
-        b = min(t1, f1);
-        if (b < a) b = a;
+    // Tiles [a, b) of this segment that row tile i (0, 1) of the item takes part in, and the positions of its rows.
+    __device__ __forceinline__ void active(const AttnParams& p, int i, int& a, int& b, int& lo, int& hi) const {
+        const int rows = s.T * p.G, r0 = rt * kTcRows + i * kTcTile, base = s.len - s.T;
+        a = b = tile0;
+        lo = pmin, hi = pmax;
+        if (r0 >= rows) return;
+        lo = base + r0 / p.G;
+        hi = base + (min(rows, r0 + kTcTile) - 1) / p.G;
+        a = max(first_tile_of(p, lo), tile0);
+        b = max(a, min(hi / kTcTile + 1, tile0 + cnt));
     }
-    __device__ __forceinline__ int first_tile(const AttnParams& p) const {
-        int t0, t1;
-        tile_range(p, s, rt * kTcRows, min(s.T * p.G, (rt + 1) * kTcRows), t0, t1);
-        return t0 + x;
-    }
-    // Whether some row of the item does not see the whole tile.
-    __device__ __forceinline__ bool edge(const AttnParams& p, int tile) const {
-        const int rows = s.T * p.G, base = s.len - s.T, k0 = tile * kTcTile;
-        const int pmin = base + rt * kTcRows / p.G, pmax = base + (min(rows, (rt + 1) * kTcRows) - 1) / p.G;
-        return k0 + kTcTile - 1 > pmin || (p.window > 0 && k0 < pmax - p.window + 1);
+    // Whether some row with a position in [lo, hi] does not see the whole tile.
+    static __device__ __forceinline__ bool edge(const AttnParams& p, int tile, int lo, int hi) {
+        const int k0 = tile * kTcTile;
+        return k0 + kTcTile - 1 > lo || (p.window > 0 && k0 < hi - p.window + 1);
     }
 };
 
@@ -293,7 +300,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             TcSeg g;
             g.start(p, c, err);
             do {
-                const int t0 = g.first_tile(p);
+                const int t0 = g.tile0;
                 const int32_t* row = p.c.table + (long long)g.n * p.c.max_pages;
                 const int pages = (g.s.len + page - 1) >> p.c.page_log2;
                 auto look = [&](int tile) {  // this lane's page of a tile: -1 behind the sequence's end
@@ -361,10 +368,10 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 TcSeg g;
                 g.start(p, c, err);
                 do {
-                    const int f0 = g.first_tile(p), f1 = f0 + g.cnt;
-                    int a[2], b[2];
-                    g.active(p, 0, a[0], b[0]);
-                    g.active(p, 1, a[1], b[1]);
+                    const int f0 = g.tile0, f1 = f0 + g.cnt;
+                    int a[2], b[2], lo, hi;
+                    g.active(p, 0, a[0], b[0], lo, hi);
+                    g.active(p, 1, a[1], b[1], lo, hi);
                     for (int i = 0; i < 2; ++i) {
                         if (ok) ok = tc_wait(&c->q_full[i], seg & 1, ab, err);
                         // a row tile without tiles here is told so too: no role gets a phase ahead of another
@@ -422,12 +429,12 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             TcSeg g;
             g.start(p, c, err);
             do {
-                const int f0 = g.first_tile(p);
+                const int f0 = g.tile0;
                 for (int j = 0; ok && j < g.cnt; ++j, ++cv) {
                     const int st = cv % L::NV;
                     ok = tc_warp_wait(&c->v_full[st], (cv / L::NV) & 1, ab, err);
                     if (!ok) break;
-                    if (g.edge(p, f0 + j)) {
+                    if (TcSeg::edge(p, f0 + j, g.pmin, g.pmax)) {
                         uint8_t* v = smem + L::OFF_V + st * L::TILE;
                         // a thread looks at two rows whole
 #pragma unroll
@@ -480,12 +487,9 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 fence_proxy_async();
                 mbar_arrive(&c->q_full[i]);
             }
-            int a, b;
-            g.active(p, i, a, b);
-            const int f0 = g.first_tile(p);
-            // this row tile's own rows: which tiles need masking
-            const int rlo = g.rt * kTcRows + i * kTcTile, rhi = min(rows, rlo + kTcTile) - 1;
-            const int pmin = g.s.len - g.s.T + rlo / p.G, pmax = g.s.len - g.s.T + rhi / p.G;
+            int a, b, plo, phi;  // this row tile's tiles and positions
+            g.active(p, i, a, b, plo, phi);
+            const int f0 = g.tile0;
             float m = -INFINITY, l = 0.f;
             for (int t = a; ok && t < b; ++t) {
                 ok = tc_warp_wait(&c->s_full[i], ns & 1, ab, err);
@@ -497,7 +501,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
                 tmem_wait_ld();
                 const int k0 = t * kTcTile;
-                if (k0 + kTcTile - 1 > pmin || (p.window > 0 && k0 < pmax - p.window + 1)) {
+                if (TcSeg::edge(p, t, plo, phi)) {
                     const int chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : -1;
 #pragma unroll
                     for (int q = 0; q < 4; ++q)
@@ -505,11 +509,17 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         for (int e = 0; e < 32; ++e)
                             if (q * 32 + e > chi || q * 32 + e < clo) s[q][e] = -INFINITY;
                 }
-                float top = -INFINITY;
+                float top;
+                {
+                    float m4[4];
 #pragma unroll
-                for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 4; ++q) {
+                        m4[q] = max3(s[q][0], s[q][1], s[q][2]);
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) top = fmaxf(top, s[q][e]);
+                        for (int e = 3; e < 31; e += 2) m4[q] = max3(m4[q], s[q][e], s[q][e + 1]);
+                    }
+                    top = max3(max3(m4[0], s[0][31], s[1][31]), max3(m4[1], s[2][31], s[3][31]), fmaxf(m4[2], m4[3]));
+                }
                 if (__any_sync(0xffffffffu, (top - m) * cs > kRescaleLog2)) {
                     const float nm = fmaxf(m, top), f = m == -INFINITY ? 0.f : exp2f((m - nm) * cs);
                     m = nm;
@@ -526,37 +536,38 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         }
                     }
                 }
-                const float mc = m == -INFINITY ? 0.f : m * cs;
-                uint32_t bad[4] = {0, 0, 0, 0};
-                int chi = 0, clo = 0;
-                if (g.edge(p, t)) {  // marked keys: see the head of the file
+                if (TcSeg::edge(p, t, g.pmin, g.pmax)) {
+                    // marked keys (see the head of the file): a row that sees one has no finite result
                     const int cv = cv0 + (t - f0), st = cv % L::NV;
                     ok = tc_warp_wait(&c->v_ready[st], (cv / L::NV) & 1, ab, err);
                     if (!ok) break;
-                    chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : 0;
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) bad[q] = c->bad[st][q];
+                    const int chi = pos - k0, clo = p.window > 0 ? max(0, chi - p.window + 1) : 0;
+#pragma unroll 1
+                    for (int q = 0; q < 4; ++q) {
+                        const int lo = clo - 32 * q, hi = chi - 32 * q;  // bits [lo, hi] of this word
+                        if (hi < 0 || lo > 31) continue;
+                        const uint32_t seen = (0xffffffffu >> (31 - min(hi, 31))) & (0xffffffffu << max(lo, 0));
+                        if (c->bad[st][q] & seen) l = __int_as_float(0x7fc00000);
+                    }
+                    __syncwarp();
                 }
-                float l4[4] = {0.f, 0.f, 0.f, 0.f};
+                const float mc = m == -INFINITY ? 0.f : m * cs;
+                const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
                     uint32_t w[16];
 #pragma unroll
-                    for (int e = 0; e < 32; e += 2) {
-                        const float x = ex2_approx(fmaf(s[q][e], cs, -mc)), y = ex2_approx(fmaf(s[q][e + 1], cs, -mc));
-                        l4[(e >> 1) & 3] += x + y;
-                        w[e >> 1] = pack_bf16x2(x, y);
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x = fma2(make_float2(s[q][2 * e], s[q][2 * e + 1]), c2, mc2);
+                        x.x = ex2_approx(x.x), x.y = ex2_approx(x.y);
+                        l2[e & 1] = add2(l2[e & 1], x);
+                        w[e] = pack_bf16x2(x.x, x.y);
                     }
-                    if (bad[q]) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (((bad[q] >> e) & 1) && q * 32 + e <= chi && q * 32 + e >= clo)
-                                w[e >> 1] = (e & 1) ? (w[e >> 1] & 0xffffu) | 0x7fc00000u : (w[e >> 1] & 0xffff0000u) | 0x7fc0u;
-                    }
-                    __syncwarp();
                     tmem_st16u(ts + q * 16, w);
                 }
-                l += (l4[0] + l4[1]) + (l4[2] + l4[3]);
+                l2[0] = add2(l2[0], l2[1]);
+                l += l2[0].x + l2[0].y;
                 tmem_wait_st();
                 tc_fence_before();
                 mbar_arrive(&c->p_full[i]);
@@ -629,9 +640,9 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         TcSeg g;
         g.start(p, c, err);
         do {
-            const int f0 = g.first_tile(p);
+            const int f0 = g.tile0;
             for (int j = 0; ok && j < g.cnt; ++j) {
-                const bool edge = g.edge(p, f0 + j);
+                const bool edge = TcSeg::edge(p, f0 + j, g.pmin, g.pmax);
                 const int valid = g.s.len - (f0 + j) * kTcTile;  // rows of the tile that are positions at all
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
