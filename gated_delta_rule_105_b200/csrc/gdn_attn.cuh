@@ -642,10 +642,11 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// A warp takes a row; its lanes hold the parts' maxima and denominators, and the first parts' sums are asked for before
-// those have arrived.  An item of the decode kernel has few rows and may have many parts (one long context shared out
-// among all CTAs): then a block takes one row, warp w its parts w, w + 8, ...
-constexpr int kJoinWarps = 8, kJoinAhead = 4;
+// Softmax parts combine like blocks do: a running maximum, sum and denominator, part after part.  An item of the chunk
+// kernel has 256 rows in few parts: a warp takes four rows at a time, with the next part's loads in flight.  One of the
+// decode kernel has few rows and may have many parts (one long context shared out among all CTAs): then a block takes one
+// row, warp w its parts w, w + 8, ..., and the warps' results combine the same way.
+constexpr int kJoinWarps = 8;
 struct JoinKernel {
     const int* desc;
     const float* part;
@@ -659,68 +660,99 @@ struct JoinParams {
     int G, hq, d, o_f32;
 };
 
-__global__ void __launch_bounds__(kJoinWarps * 32, 4) gdn_attn_join_kernel(const JoinParams p) {
-    __shared__ float4 s_a[kJoinWarps][32];
-    __shared__ float s_l[kJoinWarps];
-    cudaGridDependencySynchronize();
-    const int first = p.k[0].grid * p.k[0].blocks;
-    const bool second = (int)blockIdx.x >= first;
-    const JoinKernel k = {second ? p.k[1].desc : p.k[0].desc,   second ? p.k[1].part : p.k[0].part,
-                          second ? p.k[1].ml : p.k[0].ml,       second ? p.k[1].grid : p.k[0].grid,
-                          second ? p.k[1].rows : p.k[0].rows,   second ? p.k[1].blocks : p.k[0].blocks};
-    const int b = blockIdx.x - (second ? first : 0), c = b / k.blocks, y = b - c * k.blocks;
-    const int4 d0 = reinterpret_cast<const int4*>(k.desc)[c * 2], d1 = reinterpret_cast<const int4*>(k.desc)[c * 2 + 1];
-    if (d0.x < 0) return;
-    const int h = d0.y, row0 = d0.z, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const bool shared_row = k.blocks == k.rows && parts > kJoinWarps;
-    const int r = shared_row ? y : y * kJoinWarps + warp, i_first = shared_row ? warp : 0, step = shared_row ? kJoinWarps : 1;
-    if (r < rows) {
-        const bool mine = lane * 4 < p.d;
-        auto at = [&](int i) { return ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r; };
-        auto sums = [&](int i) {
-            return mine && i < parts ? *reinterpret_cast<const float4*>(k.part + at(i) * p.d + 4 * lane) : make_float4(0.f, 0.f, 0.f, 0.f);
-        };
-        float4 v[kJoinAhead];
-#pragma unroll
-        for (int u = 0; u < kJoinAhead; ++u) v[u] = sums(i_first + u * step);
-        float mm = -INFINITY, ll = 0.f;
-        for (int i = lane; i < parts; i += 32) mm = fmaxf(mm, k.ml[at(i) * 2]);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i0 = i_first; i0 < parts; i0 += kJoinAhead * step) {
-            float2 ml[kJoinAhead];
-#pragma unroll
-            for (int u = 0; u < kJoinAhead; ++u)
-                ml[u] = i0 + u * step < parts ? *reinterpret_cast<const float2*>(k.ml + at(i0 + u * step) * 2) : make_float2(-INFINITY, 0.f);
-#pragma unroll
-            for (int u = 0; u < kJoinAhead; ++u) {
-                const float4 x = v[u];
-                v[u] = sums(i0 + (u + kJoinAhead) * step);
-                if (ml[u].x == -INFINITY && ml[u].y == 0.f) continue;  // nothing seen there: its sums may not be written
-                const float f = ml[u].x == -INFINITY ? 1.f : exp2f(ml[u].x - mm);
-                ll += ml[u].y * f;
-                a.x += x.x * f, a.y += x.y * f, a.z += x.z * f, a.w += x.w * f;
-            }
-        }
-        if (shared_row) {
-            s_a[warp][lane] = a;
-            if (lane == 0) s_l[warp] = ll;
-            __syncthreads();
-            if (warp != 0) return;
-#pragma unroll
-            for (int w = 1; w < kJoinWarps; ++w) {
-                const float4 x = s_a[w][lane];
-                a.x += x.x, a.y += x.y, a.z += x.z, a.w += x.w;
-                ll += s_l[w];
-            }
-        }
-        const int row = row0 + r, tok = row / p.G, gh = row - tok * p.G;
-        const long long out = (long long)(start + tok) * p.hq + h * p.G + gh;
-        if (mine) attn_store4(p.o, p.o_f32, out * p.d + 4 * lane, a, ll == 0.f ? 0.f : 1.f / ll);
-        if (lane == 0 && p.lse) p.lse[out] = attn_lse(mm, ll);
+struct JoinRow {
+    float4 a;
+    float m, l;
+    __device__ __forceinline__ void add(float4 v, float vm, float vl) {
+        if (vm == -INFINITY && vl == 0.f) return;  // nothing seen there: its sums may not have been written
+        const float nm = fmaxf(m, vm);
+        // no maximum at all but a denominator: a NaN to pass on
+        const float fa = m == -INFINITY ? 0.f : exp2f(m - nm), fv = vm == -INFINITY ? 1.f : exp2f(vm - nm);
+        a.x = a.x * fa + v.x * fv, a.y = a.y * fa + v.y * fv, a.z = a.z * fa + v.z * fv, a.w = a.w * fa + v.w * fv;
+        l = l * fa + vl * fv;
+        m = nm;
     }
+};
+
+// Rows r0 .. r0 + RW - 1 (those below `rows`), parts first, first + step, ...: 4 channels a lane.
+template <int RW>
+__device__ __forceinline__ void join_rows(const JoinKernel& k, int d, int c, int slot0, int parts, int rows, int r0, int first,
+                                          int step, JoinRow (&out)[RW]) {
+    const int lane = threadIdx.x & 31;
+    const bool mine = lane * 4 < d;
+    float4 v[RW];
+    float2 ml[RW];
+    auto ask = [&](int i) {
+#pragma unroll
+        for (int u = 0; u < RW; ++u) {
+            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
+            ml[u] = make_float2(-INFINITY, 0.f);
+            if (i < parts && r0 + u < rows) {
+                const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r0 + u;
+                ml[u] = *reinterpret_cast<const float2*>(k.ml + at * 2);
+                if (mine) v[u] = *reinterpret_cast<const float4*>(k.part + at * d + 4 * lane);
+            }
+        }
+    };
+#pragma unroll
+    for (int u = 0; u < RW; ++u) out[u] = JoinRow{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    ask(first);
+    for (int i = first; i < parts; i += step) {
+        float4 x[RW];
+        float2 xm[RW];
+#pragma unroll
+        for (int u = 0; u < RW; ++u) x[u] = v[u], xm[u] = ml[u];
+        ask(i + step);
+#pragma unroll
+        for (int u = 0; u < RW; ++u) out[u].add(x[u], xm[u].x, xm[u].y);
+    }
+}
+
+__device__ __forceinline__ void join_write(const JoinParams& p, const JoinRow& r, int h, int start, int row) {
+    const int lane = threadIdx.x & 31, tok = row / p.G, gh = row - tok * p.G;
+    const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
+    if (lane * 4 < p.d) attn_store4(p.o, p.o_f32, at * p.d + 4 * lane, r.a, r.l == 0.f ? 0.f : 1.f / r.l);
+    if (lane == 0 && p.lse) p.lse[at] = attn_lse(r.m, r.l);
+}
+
+constexpr int kJoinRw = 4;
+__global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const JoinParams p) {
+    __shared__ float4 s_a[kJoinWarps][32];
+    __shared__ float2 s_ml[kJoinWarps];
+    cudaGridDependencySynchronize();
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = p.k[0].grid * p.k[0].blocks;
+    if ((int)blockIdx.x >= first) {  // chunk kernel
+        const int b = blockIdx.x - first, c = b / p.k[1].blocks, y = b - c * p.k[1].blocks;
+        const int4 d0 = reinterpret_cast<const int4*>(p.k[1].desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.k[1].desc)[c * 2 + 1];
+        if (d0.x < 0) return;
+        const int r0 = (y * kJoinWarps + warp) * kJoinRw, rows = d0.w;
+        if (r0 >= rows) return;
+        JoinRow out[kJoinRw];
+        join_rows<kJoinRw>(p.k[1], p.d, c, d1.x, d1.y, rows, r0, 0, 1, out);
+#pragma unroll
+        for (int u = 0; u < kJoinRw; ++u)
+            if (r0 + u < rows) join_write(p, out[u], d0.y, d1.z, d0.z + r0 + u);
+        return;
+    }
+    const int c = blockIdx.x / p.k[0].blocks, y = blockIdx.x - c * p.k[0].blocks;
+    const int4 d0 = reinterpret_cast<const int4*>(p.k[0].desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.k[0].desc)[c * 2 + 1];
+    if (d0.x < 0) return;
+    const int rows = d0.w, parts = d1.y;
+    const bool alone = parts <= kJoinWarps;  // a warp per row
+    const int r = alone ? y * kJoinWarps + warp : y;
+    if (r >= rows) return;
+    JoinRow out[1];
+    join_rows<1>(p.k[0], p.d, c, d1.x, parts, rows, r, alone ? 0 : warp, alone ? 1 : kJoinWarps, out);
+    if (!alone) {
+        s_a[warp][lane] = out[0].a;
+        if (lane == 0) s_ml[warp] = make_float2(out[0].m, out[0].l);
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int w = 1; w < kJoinWarps; ++w) out[0].add(s_a[w][lane], s_ml[w].x, s_ml[w].y);
+    }
+    join_write(p, out[0], d0.y, d1.z, d0.z + r);
 }
 
 }  // namespace gdn

@@ -186,7 +186,7 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
-        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, kTcRows / kJoinWarps};
+        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, kTcRows / (kJoinWarps * kJoinRw)};
     }
     const unsigned blocks = j.k[0].grid * j.k[0].blocks + j.k[1].grid * j.k[1].blocks;
     e = launch_after(gdn_attn_join_kernel, dim3(blocks), dim3(kJoinWarps * 32), 0, stream, true, j);
