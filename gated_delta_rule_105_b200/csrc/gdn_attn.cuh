@@ -9,8 +9,8 @@
 // once in blocks of 128 or 256 (a unit).  All units of all items form one line, and each CTA takes an equal stretch of it
 // whatever the sequences' lengths are: the split depends on device-side lengths only, so a captured graph replays
 // with new lengths and nothing is read back.  A CTA ends up with whole items (written directly) and at most two parts
-// of items, its first and its last, whose unnormalised sums, maxima and denominators go to the workspace; the join
-// kernel adds the parts of an item in a fixed order.  The workspace is therefore a fixed size per CTA.
+// of items, its first and its last, whose unnormalised sums, maxima and denominators go to the workspace; the parts of an
+// item are then added in a fixed order.  The workspace is therefore a fixed size per CTA.
 #pragma once
 
 #include "gdn_kv.cuh"
@@ -40,8 +40,9 @@ struct AttnParams {
     int G, hq;
     int o_f32;
     int rows_lo, rows_hi;    // this kernel takes sequences with rows_lo < T G <= rows_hi
-    int* desc;               // [grid][kDescInts]: the split item that starts in this CTA, for the join kernel
-    float* part;             // [grid][2][R][d] partial sums
+    int* desc;               // decode: [grid][kDescInts], the split item that starts in this CTA, for the join kernel;
+                             // chunk: [grid][2] finished parts of that item's row tiles, 0 at the start
+    float* part;             // [grid][2][R][d] partial sums (chunk: [grid][2][row tile][d / 4][128][4])
     float* ml;               // [grid][2][R][2] maximum (base 2) and denominator
 };
 // n (-1: none), KV head, first row, rows, slot of the first part, number of CTAs it spans
@@ -642,21 +643,18 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// Softmax parts combine like blocks do: a running maximum, sum and denominator, part after part.  An item of the chunk
-// kernel has 256 rows in few parts: a warp takes four rows at a time, with the next part's loads in flight.  One of the
-// decode kernel has few rows and may have many parts (one long context shared out among all CTAs): then a block takes one
-// row, warp w its parts w, w + 8, ..., and the warps' results combine the same way.
+// Softmax parts combine like blocks do: a running maximum, sum and denominator, part after part.  An item of the decode
+// kernel has few rows and may have many parts (one long context shared out among all CTAs): a block takes one row, warp
+// w its parts w, w + 8, ..., and the warps' results combine the same way.  (The chunk kernel's parts are joined by the
+// warpgroup that finishes the item.)
 constexpr int kJoinWarps = 8;
-struct JoinKernel {
+struct JoinParams {
     const int* desc;
     const float* part;
     const float* ml;
-    int grid, rows, blocks;  // CTAs of the attention kernel (0: not launched), its R, join blocks per CTA
-};
-struct JoinParams {
-    JoinKernel k[2];
     void* o;
     float* lse;
+    int rows;  // R of the attention kernel
     int G, hq, d, o_f32;
 };
 
@@ -674,85 +672,51 @@ struct JoinRow {
     }
 };
 
-// Rows r0 .. r0 + RW - 1 (those below `rows`), parts first, first + step, ...: 4 channels a lane.
-template <int RW>
-__device__ __forceinline__ void join_rows(const JoinKernel& k, int d, int c, int slot0, int parts, int rows, int r0, int first,
-                                          int step, JoinRow (&out)[RW]) {
-    const int lane = threadIdx.x & 31;
-    const bool mine = lane * 4 < d;
-    float4 v[RW];
-    float2 ml[RW];
-    auto ask = [&](int i) {
-#pragma unroll
-        for (int u = 0; u < RW; ++u) {
-            v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-            ml[u] = make_float2(-INFINITY, 0.f);
-            if (i < parts && r0 + u < rows) {
-                const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * k.rows + r0 + u;
-                ml[u] = *reinterpret_cast<const float2*>(k.ml + at * 2);
-                if (mine) v[u] = *reinterpret_cast<const float4*>(k.part + at * d + 4 * lane);
-            }
-        }
-    };
-#pragma unroll
-    for (int u = 0; u < RW; ++u) out[u] = JoinRow{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-    ask(first);
-    for (int i = first; i < parts; i += step) {
-        float4 x[RW];
-        float2 xm[RW];
-#pragma unroll
-        for (int u = 0; u < RW; ++u) x[u] = v[u], xm[u] = ml[u];
-        ask(i + step);
-#pragma unroll
-        for (int u = 0; u < RW; ++u) out[u].add(x[u], xm[u].x, xm[u].y);
-    }
-}
-
-__device__ __forceinline__ void join_write(const JoinParams& p, const JoinRow& r, int h, int start, int row) {
-    const int lane = threadIdx.x & 31, tok = row / p.G, gh = row - tok * p.G;
-    const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
-    if (lane * 4 < p.d) attn_store4(p.o, p.o_f32, at * p.d + 4 * lane, r.a, r.l == 0.f ? 0.f : 1.f / r.l);
-    if (lane == 0 && p.lse) p.lse[at] = attn_lse(r.m, r.l);
-}
-
-constexpr int kJoinRw = 4;
 __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const JoinParams p) {
     __shared__ float4 s_a[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
     cudaGridDependencySynchronize();
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int first = p.k[0].grid * p.k[0].blocks;
-    if ((int)blockIdx.x >= first) {  // chunk kernel
-        const int b = blockIdx.x - first, c = b / p.k[1].blocks, y = b - c * p.k[1].blocks;
-        const int4 d0 = reinterpret_cast<const int4*>(p.k[1].desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.k[1].desc)[c * 2 + 1];
-        if (d0.x < 0) return;
-        const int r0 = (y * kJoinWarps + warp) * kJoinRw, rows = d0.w;
-        if (r0 >= rows) return;
-        JoinRow out[kJoinRw];
-        join_rows<kJoinRw>(p.k[1], p.d, c, d1.x, d1.y, rows, r0, 0, 1, out);
-#pragma unroll
-        for (int u = 0; u < kJoinRw; ++u)
-            if (r0 + u < rows) join_write(p, out[u], d0.y, d1.z, d0.z + r0 + u);
-        return;
-    }
-    const int c = blockIdx.x / p.k[0].blocks, y = blockIdx.x - c * p.k[0].blocks;
-    const int4 d0 = reinterpret_cast<const int4*>(p.k[0].desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.k[0].desc)[c * 2 + 1];
+    const int c = blockIdx.x / p.rows, y = blockIdx.x - c * p.rows;
+    const int4 d0 = reinterpret_cast<const int4*>(p.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.desc)[c * 2 + 1];
     if (d0.x < 0) return;
-    const int rows = d0.w, parts = d1.y;
-    const bool alone = parts <= kJoinWarps;  // a warp per row
-    const int r = alone ? y * kJoinWarps + warp : y;
+    const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
+    const bool alone = parts <= kJoinWarps;  // few parts: a warp per row, and fewer blocks
+    const int r = alone ? y * kJoinWarps + warp : y, first = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
     if (r >= rows) return;
-    JoinRow out[1];
-    join_rows<1>(p.k[0], p.d, c, d1.x, parts, rows, r, alone ? 0 : warp, alone ? 1 : kJoinWarps, out);
+    const bool mine = lane * 4 < p.d;
+    float4 v;
+    float2 ml;
+    auto ask = [&](int i) {
+        v = make_float4(0.f, 0.f, 0.f, 0.f);
+        ml = make_float2(-INFINITY, 0.f);
+        if (i < parts) {
+            const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * p.rows + r;
+            ml = *reinterpret_cast<const float2*>(p.ml + at * 2);
+            if (mine) v = *reinterpret_cast<const float4*>(p.part + at * p.d + 4 * lane);
+        }
+    };
+    JoinRow out{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+    ask(first);
+#pragma unroll 4
+    for (int i = first; i < parts; i += step) {
+        const float4 x = v;
+        const float2 xm = ml;
+        ask(i + step);
+        out.add(x, xm.x, xm.y);
+    }
     if (!alone) {
-        s_a[warp][lane] = out[0].a;
-        if (lane == 0) s_ml[warp] = make_float2(out[0].m, out[0].l);
+        s_a[warp][lane] = out.a;
+        if (lane == 0) s_ml[warp] = make_float2(out.m, out.l);
         __syncthreads();
         if (warp != 0) return;
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) out[0].add(s_a[w][lane], s_ml[w].x, s_ml[w].y);
+        for (int w = 1; w < kJoinWarps; ++w) out.add(s_a[w][lane], s_ml[w].x, s_ml[w].y);
     }
-    join_write(p, out[0], d0.y, d1.z, d0.z + r);
+    const int row = d0.z + r, tok = row / p.G, gh = row - tok * p.G;
+    const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
+    if (mine) attn_store4(p.o, p.o_f32, at * p.d + 4 * lane, out.a, out.l == 0.f ? 0.f : 1.f / out.l);
+    if (lane == 0 && p.lse) p.lse[at] = attn_lse(out.m, out.l);
 }
 
 }  // namespace gdn

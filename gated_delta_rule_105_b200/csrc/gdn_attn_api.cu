@@ -161,6 +161,10 @@ static cudaError_t launch_decode(const AttnParams& p, int grid, unsigned* err, c
 template <int D, bool E4M3>
 static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, JoinParams& j, unsigned* err, cudaStream_t stream) {
     cudaError_t e;
+    if (plan.tc.grid) {  // the counts of finished parts
+        e = cudaMemsetAsync(ws + plan.tc.desc, 0, (size_t)plan.tc.grid * 2 * sizeof(int), stream);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel: %s", cudaGetErrorString(e));
+    }
     if (plan.dec.grid) {
         use_arrays(p, plan.dec, ws);
         p.rows_lo = 0;
@@ -168,7 +172,7 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         e = plan.dec_rows == 8 ? launch_decode<D, E4M3, 8>(p, plan.dec.grid, err, stream)
                                : launch_decode<D, E4M3, 16>(p, plan.dec.grid, err, stream);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention decode kernel launch: %s", cudaGetErrorString(e));
-        j.k[0] = {p.desc, p.part, p.ml, plan.dec.grid, plan.dec_rows, plan.dec_rows};
+        j.desc = p.desc, j.part = p.part, j.ml = p.ml, j.rows = plan.dec_rows;
     }
     if (plan.tc.grid) {
         use_arrays(p, plan.tc, ws);
@@ -184,13 +188,14 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         using L = AttnTc<D, E4M3>;
         e = allow_shared<&gdn_attn_chunk_kernel<D, E4M3>>(L::BYTES);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "cudaFuncSetAttribute: %s", cudaGetErrorString(e));
+        // beside a decode kernel it takes the SMs that that one leaves (and ends after it, for the join)
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
-        j.k[1] = {p.desc, p.part, p.ml, plan.tc.grid, kTcRows, kTcRows / (kJoinWarps * kJoinRw)};
     }
-    const unsigned blocks = j.k[0].grid * j.k[0].blocks + j.k[1].grid * j.k[1].blocks;
-    e = launch_after(gdn_attn_join_kernel, dim3(blocks), dim3(kJoinWarps * 32), 0, stream, true, j);
-    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
+    if (plan.dec.grid) {
+        e = launch_after(gdn_attn_join_kernel, dim3(plan.dec.grid * plan.dec_rows), dim3(kJoinWarps * 32), 0, stream, true, j);
+        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
+    }
     return GDN_OK;
 }
 
