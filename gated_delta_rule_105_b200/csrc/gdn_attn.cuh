@@ -456,10 +456,12 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 for (int r = 0; r < RS; ++r) {
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
-                    const float nm = fmaxf(m[r], top[r]);
-                    f[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - nm);
-                    l[r] *= f[r];
-                    m[r] = nm;
+                    f[r] = 1.f;
+                    if (top[r] > m[r] + kRescaleLog2) {  // each row by itself, whatever the others need
+                        f[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top[r]);
+                        l[r] *= f[r];
+                        m[r] = top[r];
+                    }
                 }
 #pragma unroll
                 for (int r = 0; r < RS; ++r) {

@@ -2,16 +2,18 @@
 // and how their units are shared out; here an item is 256 query rows of one (sequence, KV head) and a unit is a tile of
 // 128 keys.
 //
-// One CTA per SM.  The 256 rows are two tiles of 128 (the height of one MMA), each with its own softmax warpgroup, so
-// that one tile's softmax runs while the tensor core works for the other:
+// One CTA per SM.  The 256 rows are two tiles of 128 (the height of one MMA), each with its own softmax warpgroup.  Scores
+// come in steps of 64 keys with two buffers per row tile: S of the next step is there before the softmax of this one is
+// done, so neither the softmax nor the tensor core waits for the other's latency (with one buffer of 128 keys the softmax
+// stood still for half the time).
 //   warp 0        loads K and V tiles: one tensor-map box per (page, 64 channels), a ring of stages each
 //   warp 1        issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor memory)
 //   warps 2, 3    bf16 cache: look for non-finite V rows in tiles that are not wholly visible (see below)
-//   warps 4 - 11  softmax: thread = row, the 128 scores of a tile in registers, P back into the columns of S as bf16
+//   warps 4 - 11  softmax: thread = row, the 64 scores of a step in registers, P back into the columns of S as bf16
 //   warps 12 - 15 8-bit cache: codes of a tile (bulk copies, one per page) to exact bf16 in the swizzled layout
-// Tensor memory: S/P of both tiles (2 x 128 columns) and O of both (2 x d).  The running maximum is lazy: O is scaled
-// down only when a row's maximum has grown by more than 2^8, which after the first tiles is rare; then the warp reads
-// and writes its part of O itself (the commit that announced S came after the previous P V, so O is at rest).
+// Tensor memory: S/P of both tiles (2 x 2 x 64 columns) and O of both (2 x d).  The running maximum is lazy: O is scaled
+// down only when a row's maximum has grown by more than 2^8, which after the first steps is rare; then the warp waits for
+// the last P V and reads and writes its part of O itself.
 //
 // Masked keys.  A score that a row must not see is set to -inf before the maximum, so K may hold anything there.  For V a
 // weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, V rows with a NaN or an infinity
@@ -22,7 +24,7 @@
 
 namespace gdn {
 
-constexpr int kTcRows = 256, kTcTile = 128;
+constexpr int kTcRows = 256, kTcTile = 128, kTcStep = 64;
 
 template <int D, bool E4M3> struct AttnTc {
     static constexpr int THREADS = E4M3 ? 512 : 384;
@@ -40,7 +42,7 @@ template <int D, bool E4M3> struct AttnTc {
 
 struct AttnTcCtl {
     uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_ready[3], v_empty[3], r_full[2], r_empty[2];
-    uint64_t s_full[2], p_full[2], o_full[2], drain;
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2], drain;  // [row tile][buffer of S]
     uint32_t tmem;
     volatile int abort_flag;
     uint32_t bad[3][4];  // marked keys of each V stage's tile
@@ -95,6 +97,36 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
     return r;
 }
+// MMAs whose descriptors are given by their low words (addresses); the high words are constants.  The issuing warp walks
+// along whole, with the bases made uniform by a shuffle, so that the operands stay in uniform registers: built by one
+// thread in vector registers they cost 85 cycles an instruction, more than the tensor core takes for it.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e;
+}
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(0xffffffffu, v, 0); }
+template <uint32_t HI_A, uint32_t HI_B, uint32_t IDESC>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a, uint32_t b, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %6, p;\n\t}" ::"r"(d_tmem),
+        "r"(a), "r"(b), "r"(accumulate), "n"(HI_A), "n"(HI_B), "r"(IDESC)
+        : "memory");
+}
+template <uint32_t HI_B, uint32_t IDESC>
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 db;\n\tsetp.ne.b32 p, %3, 0;\n\tmov.b64 db, {%2, %4};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %5, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "r"(b), "r"(accumulate), "n"(HI_B), "r"(IDESC)
+        : "memory");
+}
+// Descriptor words as gdn_sm100.cuh's umma_desc() has them: address and leading offset (low), stride offset, version and
+// 128-byte swizzle (high).
+__host__ __device__ constexpr uint32_t desc_low(uint32_t saddr, uint32_t lbo) { return ((saddr >> 4) & 0x3fffu) | (lbo >> 4) << 16; }
+__host__ __device__ constexpr uint32_t desc_high(uint32_t sbo) { return (sbo >> 4) | 1u << 14 | 2u << 29; }
+
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
@@ -159,21 +191,21 @@ struct TcSeg {
         item(p, c);
         return true;
     }
-    // Tiles [a, b) of this segment that row tile i (0, 1) of the item takes part in, and the positions of its rows.
+    // Steps [a, b) of this segment that row tile i (0, 1) of the item takes part in, and the positions of its rows.
     __device__ __forceinline__ void active(const AttnParams& p, int i, int& a, int& b, int& lo, int& hi) const {
         const int rows = s.T * p.G, r0 = rt * kTcRows + i * kTcTile, base = s.len - s.T;
-        a = b = tile0;
+        constexpr int SPT = kTcTile / kTcStep;
+        a = b = tile0 * SPT;
         lo = pmin, hi = pmax;
         if (r0 >= rows) return;
         lo = base + r0 / p.G;
         hi = base + (min(rows, r0 + kTcTile) - 1) / p.G;
-        a = max(first_tile_of(p, lo), tile0);
-        b = max(a, min(hi / kTcTile + 1, tile0 + cnt));
+        a = max(p.window > 0 ? max(0, lo - p.window + 1) / kTcStep : 0, tile0 * SPT);
+        b = max(a, min(hi / kTcStep + 1, (tile0 + cnt) * SPT));
     }
-    // Whether some row with a position in [lo, hi] does not see the whole tile.
-    static __device__ __forceinline__ bool edge(const AttnParams& p, int tile, int lo, int hi) {
-        const int k0 = tile * kTcTile;
-        return k0 + kTcTile - 1 > lo || (p.window > 0 && k0 < hi - p.window + 1);
+    // Whether some row with a position in [lo, hi] does not see all keys of [k0, k0 + n).
+    static __device__ __forceinline__ bool edge(const AttnParams& p, int k0, int n, int lo, int hi) {
+        return k0 + n - 1 > lo || (p.window > 0 && k0 < hi - p.window + 1);
     }
 };
 
@@ -270,9 +302,11 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     if (tid == 0) {
         for (int i = 0; i < 2; ++i) {
             mbar_init(&c->q_full[i], 128);
-            mbar_init(&c->s_full[i], 1);
-            mbar_init(&c->p_full[i], 128);
-            mbar_init(&c->o_full[i], 1);
+            for (int j = 0; j < 2; ++j) {
+                mbar_init(&c->s_full[i][j], 1);
+                mbar_init(&c->p_full[i][j], 128);
+                mbar_init(&c->o_full[i][j], 1);
+            }
             mbar_init(&c->r_full[i], 1);
             mbar_init(&c->r_empty[i], 128);
         }
@@ -364,69 +398,102 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 }
             }
         } else if (warp == 1) {
-            // ---- MMA issuer (one thread)
-            if (lane == 0) {
-                constexpr uint32_t id_s = idesc_bf16(128, 128, false, false), id_o = idesc_bf16(128, D, false, true);
-                const uint32_t sq = smem_u32(smem + L::OFF_Q), sk = smem_u32(smem + L::OFF_K), sv = smem_u32(smem + L::OFF_V);
+            // ---- MMA issuer
+            {
+                constexpr uint32_t id_s = idesc_bf16(128, kTcStep, false, false), id_o = idesc_bf16(128, D, false, true);
+                constexpr uint32_t hi = desc_high(1024);
+                const uint32_t sq = desc_low(smem_u32(smem + L::OFF_Q), 16), sk = desc_low(smem_u32(smem + L::OFF_K), 16),
+                               sv = desc_low(smem_u32(smem + L::OFF_V), L::HALF);
                 int ck = 0, cv = 0, seg = 0;  // K and V tiles taken, segments
-                int np[2] = {0, 0};           // P tiles taken of each row tile
+                uint32_t pp = 0;              // parity of the next P, bit 2 i + buffer
                 bool ok = true;
+                auto commit = [&](uint64_t* bar) {
+                    if (elect_one()) umma_commit(bar);
+                    __syncwarp();
+                };
                 TcSeg g;
                 g.start(p, c, err);
                 do {
-                    const int f0 = g.tile0, f1 = f0 + g.cnt;
-                    int a[2], b[2], lo, hi;
-                    g.active(p, 0, a[0], b[0], lo, hi);
-                    g.active(p, 1, a[1], b[1], lo, hi);
+                    const int u0 = g.tile0 * 2, u1 = u0 + g.cnt * 2;
+                    int a[2], b[2], plo, phi;
+                    g.active(p, 0, a[0], b[0], plo, phi);
+                    g.active(p, 1, a[1], b[1], plo, phi);
+#pragma unroll
                     for (int i = 0; i < 2; ++i) {
-                        if (ok) ok = tc_wait(&c->q_full[i], seg & 1, ab, err);
-                        // a row tile without tiles here is told so too: no role gets a phase ahead of another
-                        if (ok && b[i] == a[i]) umma_commit(&c->o_full[i]);
+                        if (ok) ok = tc_warp_wait(&c->q_full[i], seg & 1, ab, err);
+                        // a row tile without steps here is told so too: no role gets a phase ahead of another
+                        if (ok && b[i] == a[i]) commit(&c->o_full[i][0]);
                     }
-                    for (int t = f0; ok && t <= f1; ++t) {
-                        // O_i += P_i V of tile t - 1, then S_i = Q_i K^T of tile t: in issue order, so S may overwrite P
-                        const int stk = ck % L::NK, stv = cv % L::NV;
-                        if (t < f1) ok = ok && tc_wait(&c->k_full[stk], (ck / L::NK) & 1, ab, err);
-                        if (t > f0) ok = ok && tc_wait(&c->v_ready[stv], (cv / L::NV) & 1, ab, err);
-                        for (int i = 0; ok && i < 2; ++i) {
-                            if (t > f0 && t - 1 >= a[i] && t - 1 < b[i]) {
-                                ok = tc_wait(&c->p_full[i], np[i]++ & 1, ab, err);
-                                if (!ok) break;
-                                tc_fence_after();
+                    // S_i of step u into buffer u & 1
+                    auto scores = [&](int i, int u) {
+                        if (u < a[i] || u >= b[i]) return;
+                        const uint32_t d = uniform(tmem + i * 128 + (u & 1) * kTcStep), q0 = uniform(sq + i * (L::TILE >> 4)),
+                                       k0 = uniform(sk + ((ck % L::NK) * L::TILE + (u & 1) * (kTcStep * 128)) / 16);
+                        uint64_t* bar = &c->s_full[i][u & 1];
+                        if (elect_one()) {
 #pragma unroll
-                                for (int ks = 0; ks < 8; ++ks)
-                                    umma_bf16_tmem_a(tmem + 256 + i * 128, tmem + i * 128 + ks * 8,
-                                                     desc_mn_sw128(sv + stv * L::TILE + ks * 2048, L::HALF), id_o, t - 1 > a[i] || ks > 0);
-                                if (t == b[i]) umma_commit(&c->o_full[i]);
+                            for (int ks = 0; ks < D / 16; ++ks) {
+                                const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) / 16;
+                                mma_ss<hi, hi, id_s>(d, q0 + off, k0 + off, ks > 0);
                             }
-                            if (t < f1 && t >= a[i] && t < b[i]) {
-                                tc_fence_after();
+                            umma_commit(bar);
+                        }
+                        __syncwarp();
+                    };
+                    ok = ok && tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
+                    if (!ok) break;
+                    tc_fence_after();
+                    for (int u = u0; u < u0 + 2; ++u) {
+                        scores(0, u);
+                        scores(1, u);
+                    }
+                    commit(&c->k_empty[ck++ % L::NK]);
+                    for (int u = u0; ok && u < u1; ++u) {
+                        // O_i += P_i V of step u, then S_i of step u + 2 into the same columns (in issue order)
+                        const int stv = cv % L::NV;
+                        if (!(u & 1)) {
+                            ok = tc_warp_wait(&c->v_ready[stv], (cv / L::NV) & 1, ab, err);
+                            if (ok && u + 2 < u1) ok = tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
+                        }
+                        const uint32_t v0 = uniform(sv + (stv * L::TILE + (u & 1) * 4 * 2048) / 16);
 #pragma unroll
-                                for (int ks = 0; ks < D / 16; ++ks) {
-                                    const uint32_t off = (ks >> 2) * L::HALF + (ks & 3) * 32;
-                                    umma_bf16(tmem + i * 128, desc_k_sw128(sq + i * L::TILE + off), desc_k_sw128(sk + stk * L::TILE + off), id_s, ks > 0);
+                        for (int i = 0; i < 2; ++i) {
+                            if (ok && u >= a[i] && u < b[i]) {
+                                const uint32_t bit = 2 * i + (u & 1);
+                                ok = tc_warp_wait(&c->p_full[i][u & 1], (pp >> bit) & 1, ab, err);
+                                if (!ok) break;
+                                pp ^= 1u << bit;
+                                tc_fence_after();
+                                const uint32_t d = uniform(tmem + 256 + i * 128), p0 = uniform(tmem + i * 128 + (u & 1) * kTcStep),
+                                               more = uniform(u > a[i]);
+                                uint64_t* bar = &c->o_full[i][u & 1];
+                                if (elect_one()) {
+#pragma unroll
+                                    for (int ks = 0; ks < kTcStep / 16; ++ks)
+                                        mma_ts<hi, id_o>(d, p0 + ks * 8, v0 + ks * (2048 / 16), ks > 0 ? 1u : more);
+                                    umma_commit(bar);
                                 }
-                                umma_commit(&c->s_full[i]);
+                                __syncwarp();
+                            }
+                            if (ok && u + 2 < u1) {
+                                tc_fence_after();
+                                scores(i, u + 2);
                             }
                         }
                         if (!ok) break;
-                        if (t > f0) {
-                            umma_commit(&c->v_empty[stv]);
+                        if (u & 1) {
+                            commit(&c->v_empty[stv]);
                             ++cv;
-                        }
-                        if (t < f1) {
-                            umma_commit(&c->k_empty[stk]);
-                            ++ck;
+                            if (u + 2 < u1) commit(&c->k_empty[ck++ % L::NK]);
                         }
                     }
                     ++seg;
                 } while (ok && g.next(p, c, err));
                 // every MMA has read its operands before the CTA goes
-                umma_commit(&c->drain);
+                commit(&c->drain);
                 int zero = 0;
-                tc_wait(&c->drain, 0, &zero, err);
+                tc_warp_wait(&c->drain, 0, &zero, err);
             }
-            __syncwarp();
         } else if (!E4M3) {
             // ---- V rows that hold a NaN or an infinity, in tiles that are not wholly visible
             const int t64 = tid - 64;
@@ -440,7 +507,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     const int st = cv % L::NV;
                     ok = tc_warp_wait(&c->v_full[st], (cv / L::NV) & 1, ab, err);
                     if (!ok) break;
-                    if (TcSeg::edge(p, f0 + j, g.pmin, g.pmax)) {
+                    if (TcSeg::edge(p, (f0 + j) * kTcTile, kTcTile, g.pmin, g.pmax)) {
                         uint8_t* v = smem + L::OFF_V + st * L::TILE;
                         // a thread looks at two rows whole
 #pragma unroll
@@ -472,7 +539,8 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         // a negative scale goes into Q's sign and a zero one into Q itself, so that larger S means larger score
         const float cs = p.scale_log2 == 0.f ? 1.f : fabsf(p.scale_log2);
         const uint32_t flip = p.scale_log2 < 0.f ? 0x80008000u : 0u, keep = p.scale_log2 == 0.f ? 0u : 0xffffffffu;
-        int ns = 0, no = 0, cv0 = 0;  // S tiles taken, segments done, V tiles before this segment
+        uint32_t sp = 0, op = 0;  // parities of the next S and of the next finished P V, a bit per buffer
+        int cv0 = 0;              // V tiles before this segment
         bool ok = true;
         TcSeg g;
         g.start(p, c, err);
@@ -493,24 +561,23 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 fence_proxy_async();
                 mbar_arrive(&c->q_full[i]);
             }
-            int a, b, plo, phi;  // this row tile's tiles and positions
+            int a, b, plo, phi;  // this row tile's steps and positions
             g.active(p, i, a, b, plo, phi);
-            const int f0 = g.tile0;
             float m = -INFINITY, l = 0.f;
-            for (int t = a; ok && t < b; ++t) {
-                ok = tc_warp_wait(&c->s_full[i], ns & 1, ab, err);
+            for (int u = a; ok && u < b; ++u) {
+                const uint32_t tb = ts + (u & 1) * kTcStep;
+                ok = tc_warp_wait(&c->s_full[i][u & 1], (sp >> (u & 1)) & 1, ab, err);
                 if (!ok) break;
-                ++ns;
+                sp ^= 1u << (u & 1);
                 tc_fence_after();
-                float s[4][32];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(ts + q * 32, s[q]);
+                float s[2][32];
+                tmem_ld32(tb, s[0]);
+                tmem_ld32(tb + 32, s[1]);
                 tmem_wait_ld();
-                const int k0 = t * kTcTile;
-                if (TcSeg::edge(p, t, plo, phi)) {
-                    const int chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : -1;
+                const int k0 = u * kTcStep, chi = pos - k0, clo = p.window > 0 ? chi - p.window + 1 : 0;
+                if (TcSeg::edge(p, k0, kTcStep, plo, phi)) {
 #pragma unroll
-                    for (int q = 0; q < 4; ++q)
+                    for (int q = 0; q < 2; ++q)
 #pragma unroll
                         for (int e = 0; e < 32; ++e)
                             if (q * 32 + e > chi || q * 32 + e < clo) s[q][e] = -INFINITY;
@@ -520,17 +587,28 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     float m4[4];
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        m4[q] = max3(s[q][0], s[q][1], s[q][2]);
+                        const float* x = &s[q >> 1][(q & 1) * 16];
+                        m4[q] = max3(x[0], x[1], x[2]);
 #pragma unroll
-                        for (int e = 3; e < 31; e += 2) m4[q] = max3(m4[q], s[q][e], s[q][e + 1]);
+                        for (int e = 3; e < 15; e += 2) m4[q] = max3(m4[q], x[e], x[e + 1]);
+                        m4[q] = fmaxf(m4[q], x[15]);
                     }
-                    top = max3(max3(m4[0], s[0][31], s[1][31]), max3(m4[1], s[2][31], s[3][31]), fmaxf(m4[2], m4[3]));
+                    top = fmaxf(max3(m4[0], m4[1], m4[2]), m4[3]);
                 }
-                if (__any_sync(0xffffffffu, (top - m) * cs > kRescaleLog2)) {
-                    const float nm = fmaxf(m, top), f = m == -INFINITY ? 0.f : exp2f((m - nm) * cs);
-                    m = nm;
-                    l *= f;
-                    if (t > a) {
+                // each row by itself: its result does not depend on the rows beside it
+                const bool grow = (top - m) * cs > kRescaleLog2;
+                if (__any_sync(0xffffffffu, grow)) {
+                    float f = 1.f;
+                    if (grow) {
+                        f = m == -INFINITY ? 0.f : exp2f((m - top) * cs);
+                        m = top;
+                        l *= f;
+                    }
+                    if (u > a) {
+                        // the step before's P V (that of the step before it is done, or S would not be here)
+                        ok = tc_warp_wait(&c->o_full[i][(u - 1) & 1], ((op >> ((u - 1) & 1)) & 1) ^ 1, ab, err);
+                        if (!ok) break;
+                        tc_fence_after();
 #pragma unroll 1
                         for (int q = 0; q < D / 16; ++q) {
                             uint32_t o[16];
@@ -542,18 +620,17 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         }
                     }
                 }
-                if (TcSeg::edge(p, t, g.pmin, g.pmax)) {
+                if (TcSeg::edge(p, (u >> 1) * kTcTile, kTcTile, g.pmin, g.pmax)) {
                     // marked keys (see the head of the file): a row that sees one has no finite result
-                    const int cv = cv0 + (t - f0), st = cv % L::NV;
+                    const int cv = cv0 + (u >> 1) - g.tile0, st = cv % L::NV;
                     ok = tc_warp_wait(&c->v_ready[st], (cv / L::NV) & 1, ab, err);
                     if (!ok) break;
-                    const int chi = pos - k0, clo = p.window > 0 ? max(0, chi - p.window + 1) : 0;
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
+                    for (int q = 0; q < 2; ++q) {
                         const int lo = clo - 32 * q, hi = chi - 32 * q;  // bits [lo, hi] of this word
                         if (hi < 0 || lo > 31) continue;
                         const uint32_t seen = (0xffffffffu >> (31 - min(hi, 31))) & (0xffffffffu << max(lo, 0));
-                        if (c->bad[st][q] & seen) l = __int_as_float(0x7fc00000);
+                        if (c->bad[st][(u & 1) * 2 + q] & seen) l = __int_as_float(0x7fc00000);
                     }
                     __syncwarp();
                 }
@@ -561,7 +638,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
+                for (int q = 0; q < 2; ++q) {
                     uint32_t w[16];
 #pragma unroll
                     for (int e = 0; e < 16; ++e) {
@@ -570,20 +647,22 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         l2[e & 1] = add2(l2[e & 1], x);
                         w[e] = pack_bf16x2(x.x, x.y);
                     }
-                    tmem_st16u(ts + q * 16, w);
+                    tmem_st16u(tb + q * 16, w);
                 }
-                l2[0] = add2(l2[0], l2[1]);
-                l += l2[0].x + l2[0].y;
                 tmem_wait_st();
                 tc_fence_before();
-                mbar_arrive(&c->p_full[i]);
+                mbar_arrive(&c->p_full[i][u & 1]);
+                op ^= 1u << (u & 1);
+                l2[0] = add2(l2[0], l2[1]);
+                l += l2[0].x + l2[0].y;
             }
             cv0 += g.cnt;
             if (!ok) break;
             // ---- the segment's result
-            ok = tc_warp_wait(&c->o_full[i], no & 1, ab, err);
+            if (b == a) op ^= 1u;  // the issuer's word that there was nothing to do
+            const int ob = b > a ? (b - 1) & 1 : 0;
+            ok = tc_warp_wait(&c->o_full[i][ob], ((op >> ob) & 1) ^ 1, ab, err);
             if (!ok) break;
-            ++no;
             tc_fence_after();
             const bool whole = g.cnt == g.units;
             const long long at = (long long)(g.s.start + tok) * p.hq + g.h * p.G + gh;
@@ -685,7 +764,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         do {
             const int f0 = g.tile0;
             for (int j = 0; ok && j < g.cnt; ++j) {
-                const bool edge = TcSeg::edge(p, f0 + j, g.pmin, g.pmax);
+                const bool edge = TcSeg::edge(p, (f0 + j) * kTcTile, kTcTile, g.pmin, g.pmax);
                 const int valid = g.s.len - (f0 + j) * kTcTile;  // rows of the tile that are positions at all
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
