@@ -7,8 +7,8 @@
 // done, so neither the softmax nor the tensor core waits for the other's latency (with one buffer of 128 keys the softmax
 // stood still for half the time).
 //   warp 0        loads K and V tiles: one tensor-map box per (page, 64 channels), a ring of stages each
-//   warp 1        issues S = Q K^T (both operands in shared memory) and O += P V (P in tensor memory)
-//   warps 2, 3    bf16 cache: look for non-finite V rows in tiles that are not wholly visible (see below)
+//   warps 1, 2    issue S = Q K^T (both operands in shared memory) and O += P V (P in tensor memory), one per row tile
+//   warp 3        bf16 cache: looks for non-finite V rows in tiles that are not wholly visible (see below)
 //   warps 4 - 11  softmax: thread = row, the 64 scores of a step in registers, P back into the columns of S as bf16
 //   warps 12 - 15 8-bit cache: codes of a tile (bulk copies, one per page) to exact bf16 in the swizzled layout
 // Tensor memory: S/P of both tiles (2 x 2 x 64 columns) and O of both (2 x d).  The running maximum is lazy: O is scaled
@@ -42,7 +42,7 @@ template <int D, bool E4M3> struct AttnTc {
 
 struct AttnTcCtl {
     uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_ready[3], v_empty[3], r_full[2], r_empty[2];
-    uint64_t s_full[2][2], p_full[2][2], o_full[2][2], drain;  // [row tile][buffer of S]
+    uint64_t s_full[2][2], p_full[2][2], o_full[2][2], drain[2];  // [row tile][buffer of S]
     uint32_t tmem;
     volatile int abort_flag;
     uint32_t bad[3][4];  // marked keys of each V stage's tile
@@ -307,18 +307,18 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 mbar_init(&c->p_full[i][j], 128);
                 mbar_init(&c->o_full[i][j], 1);
             }
+            mbar_init(&c->drain[i], 1);
             mbar_init(&c->r_full[i], 1);
             mbar_init(&c->r_empty[i], 128);
         }
         for (int i = 0; i < 3; ++i) {
             mbar_init(&c->k_full[i], E4M3 ? 128 : 1);
-            mbar_init(&c->k_empty[i], 1);
+            mbar_init(&c->k_empty[i], 2);
             mbar_init(&c->v_full[i], 1);
-            mbar_init(&c->v_ready[i], E4M3 ? 128 : 64);
-            mbar_init(&c->v_empty[i], 1);
+            mbar_init(&c->v_ready[i], E4M3 ? 128 : 32);
+            mbar_init(&c->v_empty[i], 2);
             for (int j = 0; j < 4; ++j) c->bad[i][j] = 0;
         }
-        mbar_init(&c->drain, 1);
         c->abort_flag = 0;
         fence_barrier_init();
         fence_proxy_async();
@@ -329,7 +329,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     volatile int* ab = &c->abort_flag;
 
     if (warp < 4) {
-        reg_dec<E4M3 ? 48 : 56>();
+        reg_dec<E4M3 ? 88 : 128>();
         if (warp == 0) {
             // ---- loader.  Fill f of a ring of S stages: stage f % S, waits for the (f / S)-th release.
             const int npg = kTcTile >> p.c.page_log2, page = 1 << p.c.page_log2;
@@ -397,106 +397,93 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     for (int f = max(0, fv - L::NV); f < fv; ++f) tc_wait(&c->v_full[f % L::NV], (f / L::NV) & 1, &zero, err);
                 }
             }
-        } else if (warp == 1) {
-            // ---- MMA issuer
-            {
-                constexpr uint32_t id_s = idesc_bf16(128, kTcStep, false, false), id_o = idesc_bf16(128, D, false, true);
-                constexpr uint32_t hi = desc_high(1024);
-                const uint32_t sq = desc_low(smem_u32(smem + L::OFF_Q), 16), sk = desc_low(smem_u32(smem + L::OFF_K), 16),
-                               sv = desc_low(smem_u32(smem + L::OFF_V), L::HALF);
-                int ck = 0, cv = 0, seg = 0;  // K and V tiles taken, segments
-                uint32_t pp = 0;              // parity of the next P, bit 2 i + buffer
-                bool ok = true;
-                auto commit = [&](uint64_t* bar) {
-                    if (elect_one()) umma_commit(bar);
-                    __syncwarp();
-                };
-                TcSeg g;
-                g.start(p, c, err);
-                do {
-                    const int u0 = g.tile0 * 2, u1 = u0 + g.cnt * 2;
-                    int a[2], b[2], plo, phi;
-                    g.active(p, 0, a[0], b[0], plo, phi);
-                    g.active(p, 1, a[1], b[1], plo, phi);
+        } else if (warp < 3) {
+            // ---- MMA issuers, one warp per row tile: while one waits for its P, the other's MMAs keep the tensor core busy
+            constexpr uint32_t id_s = idesc_bf16(128, kTcStep, false, false), id_o = idesc_bf16(128, D, false, true);
+            constexpr uint32_t hi = desc_high(1024);
+            const int i = warp - 1;
+            const uint32_t sq = uniform(desc_low(smem_u32(smem + L::OFF_Q + i * L::TILE), 16)),
+                           ts = uniform(tmem + i * 128), to = uniform(tmem + 256 + i * 128);
+            const uint32_t sk = desc_low(smem_u32(smem + L::OFF_K), 16), sv = desc_low(smem_u32(smem + L::OFF_V), L::HALF);
+            int ck = 0, cv = 0, seg = 0;  // K and V tiles taken, segments
+            uint32_t pp = 0;              // parity of the next P, a bit per buffer
+            bool ok = true;
+            // S = Q K^T of 64 keys into buffer h, O += P V of buffer h (by one lane)
+            auto scores = [&](int h, uint32_t k0) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        if (ok) ok = tc_warp_wait(&c->q_full[i], seg & 1, ab, err);
+                for (int ks = 0; ks < D / 16; ++ks) {
+                    const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) / 16;
+                    mma_ss<hi, hi, id_s>(ts + h * kTcStep, sq + off, k0 + h * (kTcStep * 128 / 16) + off, ks > 0);
+                }
+                umma_commit(&c->s_full[i][h]);
+            };
+            auto values = [&](int h, uint32_t v0, uint32_t more) {
+#pragma unroll
+                for (int ks = 0; ks < kTcStep / 16; ++ks)
+                    mma_ts<hi, id_o>(to, ts + h * kTcStep + ks * 8, v0 + (h * 4 + ks) * (2048 / 16), ks > 0 ? 1u : more);
+                umma_commit(&c->o_full[i][h]);
+            };
+            TcSeg g;
+            g.start(p, c, err);
+            do {
+                const int u0 = g.tile0 * 2, tiles = g.cnt;
+                int a, b, plo, phi;
+                g.active(p, i, a, b, plo, phi);
+                ok = tc_warp_wait(&c->q_full[i], seg & 1, ab, err) && tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
+                if (!ok) break;
+                tc_fence_after();
+                {
+                    const uint32_t k0 = uniform(sk + (ck % L::NK) * (L::TILE / 16));
+                    if (elect_one()) {
                         // a row tile without steps here is told so too: no role gets a phase ahead of another
-                        if (ok && b[i] == a[i]) commit(&c->o_full[i][0]);
-                    }
-                    // S_i of step u into buffer u & 1
-                    auto scores = [&](int i, int u) {
-                        if (u < a[i] || u >= b[i]) return;
-                        const uint32_t d = uniform(tmem + i * 128 + (u & 1) * kTcStep), q0 = uniform(sq + i * (L::TILE >> 4)),
-                                       k0 = uniform(sk + ((ck % L::NK) * L::TILE + (u & 1) * (kTcStep * 128)) / 16);
-                        uint64_t* bar = &c->s_full[i][u & 1];
-                        if (elect_one()) {
+                        if (b == a) umma_commit(&c->o_full[i][0]);
 #pragma unroll
-                            for (int ks = 0; ks < D / 16; ++ks) {
-                                const uint32_t off = ((ks >> 2) * L::HALF + (ks & 3) * 32) / 16;
-                                mma_ss<hi, hi, id_s>(d, q0 + off, k0 + off, ks > 0);
+                        for (int h = 0; h < 2; ++h)
+                            if (u0 + h >= a && u0 + h < b) scores(h, k0);
+                        umma_commit(&c->k_empty[ck % L::NK]);
+                    }
+                    __syncwarp();
+                    ++ck;
+                }
+                for (int t = 0; ok && t < tiles; ++t) {
+                    // Of each step u: O += P V of u, then S of u + 2 into the same columns (in issue order).
+                    const int stv = cv % L::NV, stk = ck % L::NK;
+                    const bool more = t + 1 < tiles;
+                    ok = tc_warp_wait(&c->v_ready[stv], (cv / L::NV) & 1, ab, err);
+                    if (ok && more) ok = tc_warp_wait(&c->k_full[stk], (ck / L::NK) & 1, ab, err);
+                    const uint32_t v0 = uniform(sv + stv * (L::TILE / 16)), k0 = uniform(sk + stk * (L::TILE / 16));
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const int u = u0 + 2 * t + h;
+                        const bool pv = u >= a && u < b, qk = more && u + 2 >= a && u + 2 < b;
+                        if (ok && pv) {
+                            ok = tc_warp_wait(&c->p_full[i][h], (pp >> h) & 1, ab, err);
+                            pp ^= 1u << h;
+                        }
+                        if (!ok) continue;
+                        tc_fence_after();
+                        if (elect_one()) {
+                            if (pv) values(h, v0, u > a);
+                            if (qk) scores(h, k0);
+                            if (h == 1) {
+                                umma_commit(&c->v_empty[stv]);
+                                if (more) umma_commit(&c->k_empty[stk]);
                             }
-                            umma_commit(bar);
                         }
                         __syncwarp();
-                    };
-                    ok = ok && tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
-                    if (!ok) break;
-                    tc_fence_after();
-                    for (int u = u0; u < u0 + 2; ++u) {
-                        scores(0, u);
-                        scores(1, u);
                     }
-                    commit(&c->k_empty[ck++ % L::NK]);
-                    for (int u = u0; ok && u < u1; ++u) {
-                        // O_i += P_i V of step u, then S_i of step u + 2 into the same columns (in issue order)
-                        const int stv = cv % L::NV;
-                        if (!(u & 1)) {
-                            ok = tc_warp_wait(&c->v_ready[stv], (cv / L::NV) & 1, ab, err);
-                            if (ok && u + 2 < u1) ok = tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
-                        }
-                        const uint32_t v0 = uniform(sv + (stv * L::TILE + (u & 1) * 4 * 2048) / 16);
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            if (ok && u >= a[i] && u < b[i]) {
-                                const uint32_t bit = 2 * i + (u & 1);
-                                ok = tc_warp_wait(&c->p_full[i][u & 1], (pp >> bit) & 1, ab, err);
-                                if (!ok) break;
-                                pp ^= 1u << bit;
-                                tc_fence_after();
-                                const uint32_t d = uniform(tmem + 256 + i * 128), p0 = uniform(tmem + i * 128 + (u & 1) * kTcStep),
-                                               more = uniform(u > a[i]);
-                                uint64_t* bar = &c->o_full[i][u & 1];
-                                if (elect_one()) {
-#pragma unroll
-                                    for (int ks = 0; ks < kTcStep / 16; ++ks)
-                                        mma_ts<hi, id_o>(d, p0 + ks * 8, v0 + ks * (2048 / 16), ks > 0 ? 1u : more);
-                                    umma_commit(bar);
-                                }
-                                __syncwarp();
-                            }
-                            if (ok && u + 2 < u1) {
-                                tc_fence_after();
-                                scores(i, u + 2);
-                            }
-                        }
-                        if (!ok) break;
-                        if (u & 1) {
-                            commit(&c->v_empty[stv]);
-                            ++cv;
-                            if (u + 2 < u1) commit(&c->k_empty[ck++ % L::NK]);
-                        }
-                    }
-                    ++seg;
-                } while (ok && g.next(p, c, err));
-                // every MMA has read its operands before the CTA goes
-                commit(&c->drain);
-                int zero = 0;
-                tc_warp_wait(&c->drain, 0, &zero, err);
-            }
+                    ++cv;
+                    if (more) ++ck;
+                }
+                ++seg;
+            } while (ok && g.next(p, c, err));
+            // every MMA has read its operands before the CTA goes
+            if (elect_one()) umma_commit(&c->drain[i]);
+            __syncwarp();
+            int zero = 0;
+            tc_warp_wait(&c->drain[i], 0, &zero, err);
         } else if (!E4M3) {
             // ---- V rows that hold a NaN or an infinity, in tiles that are not wholly visible
-            const int t64 = tid - 64;
             int cv = 0;
             bool ok = true;
             TcSeg g;
@@ -509,10 +496,10 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     if (!ok) break;
                     if (TcSeg::edge(p, (f0 + j) * kTcTile, kTcTile, g.pmin, g.pmax)) {
                         uint8_t* v = smem + L::OFF_V + st * L::TILE;
-                        // a thread looks at two rows whole
-#pragma unroll
-                        for (int rr = 0; rr < 2; ++rr) {
-                            const int r = t64 + 64 * rr;
+                        // a thread looks at four rows whole
+#pragma unroll 1
+                        for (int rr = 0; rr < 4; ++rr) {
+                            const int r = lane + 32 * rr;
                             bool bad = false;
                             for (int ch = 0; ch < D / 8; ++ch) {
                                 const uint4 u = *reinterpret_cast<const uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7));
@@ -522,7 +509,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                                 for (int ch = 0; ch < D / 8; ++ch)
                                     *reinterpret_cast<uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
                             const uint32_t m = __ballot_sync(0xffffffffu, bad);
-                            if (lane == 0) c->bad[st][(r >> 5)] = m;
+                            if (lane == 0) c->bad[st][rr] = m;
                         }
                         fence_proxy_async();
                     }
@@ -532,7 +519,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         }
     } else if (warp < 12) {
         // ---- softmax
-        reg_inc<E4M3 ? 192 : 216>();
+        reg_inc<E4M3 ? 168 : 184>();
         const int i = (warp - 4) >> 2, r = (warp & 3) * 32 + lane;  // row tile, row in it
         const uint32_t ts = tmem + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
         const uint32_t to = tmem + 256 + i * 128 + ((uint32_t)((warp & 3) * 32) << 16);
@@ -753,7 +740,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         } while (ok && g.next(p, c, err));
     } else {
         // ---- 8-bit cache: codes to bf16.  Eight (D = 64: four) threads share a row, 16 codes each.
-        reg_dec<80>();
+        reg_dec<88>();
         const int t128 = tid - 384;
         constexpr int TPR = D / 16, RPP = 128 / TPR;  // threads of a row, rows per pass
         const int col = t128 % TPR, r_in = t128 / TPR;
