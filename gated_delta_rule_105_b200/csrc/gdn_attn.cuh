@@ -29,21 +29,6 @@ namespace gdn {
 
 constexpr int kAttnSms = 148;  // B200
 
-// Division of x in [0, 2^31) by a number that the host knows: with 2^(l-1) < d <= 2^l and m = ceil(2^(31+l) / d), the product
-// x m >> (31 + l) is floor(x / d) (m's excess over 2^(31+l) / d is below 1, hence the quotient's below 2^-l <= 1 / d).
-struct FastDiv {
-    uint32_t m;
-    int shift, d;
-    __host__ __device__ FastDiv() : m(0), shift(0), d(1) {}
-    explicit FastDiv(int n) : d(n) {
-        int l = 0;
-        while ((1 << l) < n) ++l;
-        shift = 31 + l;
-        m = (uint32_t)(((1ull << shift) + n - 1) / n);
-    }
-    __device__ __forceinline__ int div(int x) const { return (int)(((unsigned long long)(uint32_t)x * m) >> shift); }
-};
-
 struct AttnParams {
     KvParams c;
     const __nv_bfloat16* q;  // [n_tok][hq][d], token rows q_stride elements apart
@@ -53,7 +38,6 @@ struct AttnParams {
     float scale_log2;        // scale * log2(e)
     int window;              // 0: none
     int G, hq;
-    FastDiv per_g;  // division by G
     int o_f32;
     int rows_lo, rows_hi;    // this kernel takes sequences with rows_lo < T G <= rows_hi
     int* desc;               // decode: [grid][kDescInts], the split item that starts in this CTA, for the join kernel;
@@ -276,7 +260,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
         for (int r = 0; r < RS; ++r) {
             const int row = row_lo + 8 * r;
             const bool there = row < rows;
-            const int tok = there ? p.per_g.div(row) : 0, gh = there ? row - tok * p.G : 0;
+            const int tok = there ? row / p.G : 0, gh = there ? row - tok * p.G : 0;
             const int pos = len - T + tok;
             hi_[r] = there ? pos : -1;
             lo_[r] = p.window > 0 ? pos - p.window + 1 : 0;
@@ -631,7 +615,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 ll += s_ml[(ww * R + r) * 2 + 1] * (mw == -INFINITY ? 1.f : exp2f(mw - mm));
             }
             if (whole) {
-                const int tok = p.per_g.div(row), gh = row - tok * p.G;
+                const int tok = row / p.G, gh = row - tok * p.G;
                 const long long at = (long long)(sp.s.start + tok) * p.hq + h * p.G + gh;
                 attn_store4(p.o, p.o_f32, at * D + d, a, ll == 0.f ? 0.f : 1.f / ll);
                 if (d == 0 && p.lse) p.lse[at] = attn_lse(mm, ll);

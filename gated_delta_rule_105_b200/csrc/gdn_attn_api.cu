@@ -343,7 +343,7 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
                               int Hkv, int d, gdn_dtype cache_dt, gdn_dtype o_dt, void* workspace, size_t ws_bytes,
                               cudaStream_t stream) {
     clear_error();
-    AttnParams p{};
+    AttnParams p = {};
     gdn_status st = check_cache(&p.c, k_cache, v_cache, k_scale, v_scale, block_table, n_tok, n_seqs, n_pages, max_pages,
                                 page_size, Hkv, d, cache_dt);
     if (st != GDN_OK) return st;
@@ -372,7 +372,6 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     p.scale_log2 = scale * kLog2e;
     p.window = window;
     p.G = Hq / Hkv;
-    p.per_g = FastDiv(p.G);
     p.hq = Hq;
     p.o_f32 = o_dt == GDN_F32;
     uint8_t* ws = static_cast<uint8_t*>(workspace);

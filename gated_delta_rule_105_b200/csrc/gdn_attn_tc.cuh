@@ -47,8 +47,8 @@ struct AttnTcCtl {
     volatile int abort_flag;
     uint32_t bad[3][4];  // marked keys of each V stage's tile
     // where this CTA's stretch starts
-    long long quot, w0, w1;
-    int rest, grid, n, h, rt, x;
+    long long W, w0, w1;
+    int n, h, rt, x;
     int ticket[2];
 };
 static_assert(sizeof(AttnTcCtl) <= 1024, "control block");
@@ -130,14 +130,16 @@ __host__ __device__ constexpr uint32_t desc_high(uint32_t sbo) { return (sbo >> 
 template <int N> __device__ __forceinline__ void reg_inc() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void reg_dec() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 
-// First tile that a row at position `pos` sees.
-__device__ __forceinline__ int tc_first_tile(const AttnParams& p, int pos) {
-    return p.window > 0 ? max(0, pos - p.window + 1) / kTcTile : 0;
+// Key tiles [t0, t1) that rows [r0, r1) of a sequence see (r0 < r1 <= rows).
+__device__ __forceinline__ void tile_range(const AttnParams& p, const SeqSpan& s, int r0, int r1, int& t0, int& t1) {
+    const int base = s.len - s.T;
+    t1 = (base + (r1 - 1) / p.G) / kTcTile + 1;
+    t0 = p.window > 0 ? max(0, base + r0 / p.G - p.window + 1) / kTcTile : 0;
 }
-// Tiles of row group rt of a sequence.
 __device__ __forceinline__ int tc_units(const AttnParams& p, const SeqSpan& s, int rt) {
-    const int base = s.len - s.T, last = min(s.T * p.G, (rt + 1) * kTcRows) - 1;
-    return (base + p.per_g.div(last)) / kTcTile + 1 - tc_first_tile(p, base + p.per_g.div(rt * kTcRows));
+    int t0, t1;
+    tile_range(p, s, rt * kTcRows, min(s.T * p.G, (rt + 1) * kTcRows), t0, t1);
+    return t1 - t0;
 }
 // The sequence's span if this kernel takes it, T = 0 if not.
 __device__ __forceinline__ SeqSpan tc_span(const AttnParams& p, int n, unsigned* err) {
@@ -156,12 +158,15 @@ struct TcSeg {
 
     __device__ __forceinline__ void item(const AttnParams& p, const AttnTcCtl* c) {
         const int rows = s.T * p.G, base = s.len - s.T;
-        pmin = base + p.per_g.div(rt * kTcRows);
-        pmax = base + p.per_g.div(min(rows, (rt + 1) * kTcRows) - 1);
-        const int first = tc_first_tile(p, pmin);
+        pmin = base + rt * kTcRows / p.G;
+        pmax = base + (min(rows, (rt + 1) * kTcRows) - 1) / p.G;
+        const int first = first_tile_of(p, pmin);
         units = pmax / kTcTile + 1 - first;
         tile0 = first + x;
         cnt = (int)min((long long)(units - x), c->w1 - w);
+    }
+    static __device__ __forceinline__ int first_tile_of(const AttnParams& p, int pos) {
+        return p.window > 0 ? max(0, pos - p.window + 1) / kTcTile : 0;
     }
     __device__ __forceinline__ void start(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
         n = c->n, h = c->h, rt = c->rt, x = c->x, w = c->w0;
@@ -193,8 +198,8 @@ struct TcSeg {
         a = b = tile0 * SPT;
         lo = pmin, hi = pmax;
         if (r0 >= rows) return;
-        lo = base + p.per_g.div(r0);
-        hi = base + p.per_g.div(min(rows, r0 + kTcTile) - 1);
+        lo = base + r0 / p.G;
+        hi = base + (min(rows, r0 + kTcTile) - 1) / p.G;
         a = max(p.window > 0 ? max(0, lo - p.window + 1) / kTcStep : 0, tile0 * SPT);
         b = max(a, min(hi / kTcStep + 1, (tile0 + cnt) * SPT));
     }
@@ -204,54 +209,40 @@ struct TcSeg {
     }
 };
 
-// The stretch of CTA c begins at unit tc_bound(c) of W = quot * grid + rest.
-__device__ __forceinline__ long long tc_bound(const AttnTcCtl* c, int cta) { return c->quot * cta + (long long)(c->rest * cta / c->grid); }
-// The CTA whose stretch holds unit w.
-__device__ __forceinline__ int tc_owner(const AttnTcCtl* c, long long w) {
-    int cta = (int)min((long long)c->grid - 1, w / c->quot);  // too high at most by the rest's share (quot >= 1)
-    while (tc_bound(c, cta) > w) --cta;
-    return cta;
-}
 // Workspace slot of part k of an item that starts at unit `from` in CTA `owner`: a CTA has two, for the part that its
 // stretch begins with and for another one at its end.
-__device__ __forceinline__ long long tc_slot(const AttnTcCtl* c, int owner, int k, long long from) {
-    return (owner + k) * 2LL + (k == 0 && tc_bound(c, owner) != from ? 1 : 0);
+__device__ __forceinline__ long long tc_slot(long long W, long long grid, int owner, int k, long long from) {
+    return (owner + k) * 2LL + (k == 0 && W * owner / grid != from ? 1 : 0);
 }
 
 // Shares out the units and finds this CTA's first segment; false: nothing to do.  All threads.
 template <int THREADS>
 __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, TcScratch* sc, unsigned* err) {
     const int tid = threadIdx.x, N = p.c.n_seq;
-    int k = 0;  // log2 of the threads per sequence
-    while (k < 8 && (2 << k) * N <= 256) ++k;
-    const int per = 256 >> k;
+    int k = 1;  // threads per sequence
+    while (k < 256 && k * 2 * N <= 256) k *= 2;
+    const int per = 256 / k;
     auto mine_of = [&](int base) {
         long long mine = 0;
-        const int n = base + (tid >> k);
+        const int n = base + tid / k;
         if (tid < 256 && n < N) {
             const SeqSpan s = tc_span(p, n, err);
             const int rts = (s.T * p.G + kTcRows - 1) / kTcRows;
-            for (int rt = tid & ((1 << k) - 1); rt < rts; rt += 1 << k) mine += tc_units(p, s, rt);
+            for (int rt = tid % k; rt < rts; rt += k) mine += tc_units(p, s, rt);
         }
         return mine * p.c.hkv;
     };
-    long long W = 0, total = 0, before = 0;
-    for (int base = 0; base < N; base += per) {  // once, for up to 256 sequences
-        before = block_scan<THREADS>(mine_of(base), total, sc->scan);
+    long long W = 0, total;
+    for (int base = 0; base < N; base += per) {
+        block_scan<THREADS>(mine_of(base), total, sc->scan);
         W += total;
     }
     const int grid = (int)min((long long)gridDim.x, W), cta = blockIdx.x;
     if (cta >= grid) return false;
-    if (tid == 0) {
-        c->quot = W / grid;
-        c->rest = (int)(W - c->quot * grid);
-        c->grid = grid;
-    }
-    __syncthreads();
-    const long long w0 = tc_bound(c, cta), w1 = tc_bound(c, cta + 1);
+    const long long w0 = W * cta / grid, w1 = W * (cta + 1) / grid;
     long long seen = 0;
     for (int base = 0; base < N; base += per) {
-        if (N > per) before = block_scan<THREADS>(mine_of(base), total, sc->scan);
+        const long long before = block_scan<THREADS>(mine_of(base), total, sc->scan);
         if (seen + total <= w0) {
             seen += total;
             continue;
@@ -259,10 +250,10 @@ __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, T
         if (tid < 256) sc->pre[tid] = seen + before;
         if (tid == 0) sc->pre[256] = seen + total;
         __syncthreads();
-        if (tid < 256 && (tid & ((1 << k) - 1)) == 0 && sc->pre[tid] <= w0 && w0 < sc->pre[tid + (1 << k)]) {
-            c->n = base + (tid >> k);
-            c->w0 = sc->pre[tid];  // for now: where the sequence starts
-            c->w1 = sc->pre[tid + (1 << k)] - sc->pre[tid];
+        if (tid < 256 && tid % k == 0 && sc->pre[tid] <= w0 && w0 < sc->pre[tid + k]) {
+            c->n = base + tid / k;
+            c->w0 = sc->pre[tid];        // for now: where the sequence starts
+            c->w1 = sc->pre[tid + k] - sc->pre[tid];
         }
         break;
     }
@@ -277,16 +268,16 @@ __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, T
     for (int base = 0; base < rts; base += THREADS) {
         const int rt = base + tid;
         const int u = rt < rts ? tc_units(p, s, rt) : 0;
-        const long long first = at + block_scan<THREADS>(u, total, sc->scan);
-        if (u > 0 && first <= rem && rem < first + u) {
+        const long long before = at + block_scan<THREADS>(u, total, sc->scan);
+        if (u > 0 && before <= rem && rem < before + u) {
             c->rt = rt;
-            c->x = (int)(rem - first);
+            c->x = (int)(rem - before);
         }
         at += total;
         if (at > rem) break;
     }
     __syncthreads();
-    if (tid == 0) c->h = h, c->w0 = w0, c->w1 = w1;
+    if (tid == 0) c->h = h, c->W = W, c->w0 = w0, c->w1 = w1;
     __syncthreads();
     return true;
 }
@@ -543,7 +534,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
         do {
             const int rows = g.s.T * p.G, row = g.rt * kTcRows + i * kTcTile + r;
             const bool there = row < rows;
-            const int tok = there ? p.per_g.div(row) : 0, gh = row - tok * p.G;
+            const int tok = there ? row / p.G : 0, gh = row - tok * p.G;
             const int pos = g.s.len - g.s.T + tok;
             {
                 const uint4* q = reinterpret_cast<const uint4*>(p.q + (long long)(g.s.start + tok) * p.q_stride + (long long)(g.h * p.G + (there ? gh : 0)) * D);
@@ -666,12 +657,13 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             // A part of an item is left in the workspace for whichever warpgroup finishes the item's last part; that one
             // adds all parts in their order (so the result does not depend on which it is).
             bool last = whole;
-            int owner = 0, parts = 1;
-            const long long from = g.w - g.x;
+            int owner = 0, parts = 1, mine = 0;
             if (!whole) {
-                owner = tc_owner(c, from);
-                parts = tc_owner(c, from + g.units - 1) - owner + 1;
-                const long long slot = tc_slot(c, owner, (int)blockIdx.x - owner, from);
+                const long long grid = min((long long)gridDim.x, c->W), from = g.w - g.x;
+                owner = (int)(((from + 1) * grid + c->W - 1) / c->W) - 1;  // the CTA whose stretch holds the item's first tile
+                parts = (int)(((from + g.units) * grid + c->W - 1) / c->W) - owner;
+                mine = (int)blockIdx.x - owner;
+                const long long slot = tc_slot(c->W, grid, owner, mine, from);
                 if (there) reinterpret_cast<float2*>(p.ml)[slot * kTcRows + i * kTcTile + r] = make_float2(m2, l);
                 if (b > a) {
                     float4* dst = reinterpret_cast<float4*>(p.part) + (slot * 2 + i) * (D / 4) * kTcTile + r;
@@ -695,14 +687,15 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
             if (last) {
                 float mm = m2, ll = l;
-                const float2* ml = reinterpret_cast<const float2*>(p.ml) + i * kTcTile + r;
+                const long long grid = min((long long)gridDim.x, c->W), from = g.w - g.x;
                 if (!whole) {
                     mm = -INFINITY, ll = 0.f;
-#pragma unroll 4
-                    for (int k = 0; k < parts; ++k) mm = fmaxf(mm, __ldcg(ml + tc_slot(c, owner, k, from) * kTcRows).x);
-#pragma unroll 4
                     for (int k = 0; k < parts; ++k) {
-                        const float2 v = __ldcg(ml + tc_slot(c, owner, k, from) * kTcRows);
+                        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml) + tc_slot(c->W, grid, owner, k, from) * kTcRows + i * kTcTile + r);
+                        if (there && v.x > mm) mm = v.x;
+                    }
+                    for (int k = 0; k < parts; ++k) {
+                        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml) + tc_slot(c->W, grid, owner, k, from) * kTcRows + i * kTcTile + r);
                         ll += v.y * (v.x == -INFINITY ? 1.f : exp2f(v.x - mm));
                     }
                 }
@@ -717,32 +710,22 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     } else {
 #pragma unroll
                         for (int e = 0; e < 32; ++e) o[e] = 0.f;
-#pragma unroll 1
-                        for (int k = 0; k < parts; ++k) {
-                            const long long slot = tc_slot(c, owner, k, from);
-                            const float2 x = __ldcg(ml + slot * kTcRows);
-                            // (a part that has seen nothing may not have written its sums)
-                            const bool has = there && !(x.x == -INFINITY && x.y == 0.f);
-                            const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - mm);
-                            float v[32];
-                            if (owner + k == (int)blockIdx.x) {  // this warpgroup's own: still in tensor memory
-                                if (b > a) {
-                                    tmem_ld32(to + q * 32, v);
-                                    tmem_wait_ld();
-                                }
-                            } else if (has) {
+                        if (there) {
+                            for (int k = 0; k < parts; ++k) {
+                                const long long slot = tc_slot(c->W, grid, owner, k, from);
+                                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + slot * kTcRows + i * kTcTile + r);
+                                if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen there: its sums may not be written
+                                const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mm);
                                 const float4* src = reinterpret_cast<const float4*>(p.part) + ((slot * 2 + i) * (D / 4) + q * 8) * kTcTile + r;
 #pragma unroll
                                 for (int e = 0; e < 8; ++e) {
-                                    const float4 y = __ldcg(src + e * kTcTile);
-                                    v[4 * e] = y.x, v[4 * e + 1] = y.y, v[4 * e + 2] = y.z, v[4 * e + 3] = y.w;
+                                    const float4 v = __ldcg(src + e * kTcTile);
+                                    o[4 * e] = fmaf(v.x, f, o[4 * e]);
+                                    o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
+                                    o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
+                                    o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
                                 }
                             }
-                            if (has) {
-#pragma unroll
-                                for (int e = 0; e < 32; ++e) o[e] = fmaf(v[e], f, o[e]);
-                            }
-                            __syncwarp();
                         }
                     }
                     if (there) {
