@@ -89,6 +89,24 @@ __device__ __forceinline__ int kv_warp_find(const int32_t* cu, int n_seq, int ta
     return lo;
 }
 
+// The same for the rows tau0 .. tau0 + nt - 1 (nt <= TPW) of a warp: lane t < nt gets row tau0 + t's sequence, n = -1 where it
+// has none.
+template <int TPW>
+__device__ __forceinline__ void kv_warp_find_rows(const int32_t* cu, int n_seq, int tau0, int nt, int& n, int& start, int& end, unsigned* err) {
+    int cn = -1, cs = 0, ce = 0;
+    if (TPW == 1) {  // (every lane)
+        n = kv_warp_find(cu, n_seq, tau0, start, end, err);
+        return;
+    }
+    n = -1;
+#pragma unroll
+    for (int t = 0; t < TPW; ++t) {
+        if (t >= nt) break;
+        if (cn < 0 || tau0 + t >= ce) cn = kv_warp_find(cu, n_seq, tau0 + t, cs, ce, err);
+        if ((threadIdx.x & 31) == t) n = cn, start = cs, end = ce;
+    }
+}
+
 // Page index of block-table entry i of sequence n, or -1 (error word set) when it names no page of the pool.
 __device__ __forceinline__ int kv_page(const KvParams& p, int n, int i, unsigned* err) {
     const int pg = p.table[(long long)n * p.max_pages + i];
@@ -201,56 +219,66 @@ __device__ __forceinline__ void kv_store_row(const KvParams& c, int which, long 
     }
 }
 
-constexpr int kKvWarps = 8;
+constexpr int kKvWarps = 8, kKvBatch = 4;  // loads of K, and of V, that a lane has in flight
 
-// One warp per new token.  Its K and V rows are loaded before the token's place in the cache is known (the search
-// over cu_seqlens, the length and the block table are a chain of dependent loads that does not need them).  LG
+// One warp per TPW new tokens.  Their first K and V rows are loaded before the tokens' places in the cache are known (the
+// search over cu_seqlens, the length and the block table are a chain of dependent loads that does not need them).  LG
 // lanes hold one head's row, so the row maximum is log2(LG) shuffles and each head's codes leave as full sectors.
-template <typename TIn, int D, bool E4M3>
+template <typename TIn, int D, bool E4M3, int TPW>
 __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_append_kernel(const KvAppendParams p, unsigned* err) {
-    constexpr int N = Vec16<TIn>::N, LG = D / N, RPP = 32 / LG, PB = 4;  // rows per pass, passes per batch
+    constexpr int N = Vec16<TIn>::N, LG = D / N, RPP = 32 / LG, PB = kKvBatch;  // rows per pass, passes per batch
     const int lane = threadIdx.x & 31;
-    const int tau = blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-    if (tau >= p.c.n_tok) return;
-    const int hkv = p.c.hkv, sub = lane / LG, col = lane % LG;
-    const uint4* src[2];
+    const int tau0 = (blockIdx.x * kKvWarps + (threadIdx.x >> 5)) * TPW, ntok = min(TPW, p.c.n_tok - tau0);
+    if (ntok <= 0) return;
+    const int tl = TPW == 1 ? 0 : lane;  // the token that this lane looks up
+    // row r of the warp's ntok * hkv is head r mod hkv of token r / hkv
+    const int hkv = p.c.hkv, nr = ntok * hkv, sub = lane / LG, col = lane % LG;
+    auto token_of = [&](int r) {
+        int t = 0;
 #pragma unroll
-    for (int w = 0; w < 2; ++w)
-        src[w] = reinterpret_cast<const uint4*>(static_cast<const TIn*>(p.x[w]) + (long long)tau * p.stride[w]) + lane;
+        for (int i = 1; i < TPW; ++i) t += r >= i * hkv;
+        return t;
+    };
     uint4 u[2][PB];
-    auto load = [&](int h0) {
+    auto load = [&](int r0) {
 #pragma unroll
-        for (int b = 0; b < PB; ++b)
+        for (int b = 0; b < PB; ++b) {
+            const int r = r0 + b * RPP + sub, t = token_of(r);
 #pragma unroll
             for (int w = 0; w < 2; ++w)
-                u[w][b] = h0 + b * RPP + sub < hkv ? src[w][(h0 / RPP + b) * 32] : make_uint4(0, 0, 0, 0);
+                u[w][b] = r < nr ? *(reinterpret_cast<const uint4*>(static_cast<const TIn*>(p.x[w]) + (tau0 + t) * p.stride[w]) +
+                                     (r - t * hkv) * LG + col)
+                                 : make_uint4(0, 0, 0, 0);
+        }
     };
     load(0);
     int n, start, end;
     if (p.c.cu) {
-        n = kv_warp_find(p.c.cu, p.c.n_seq, tau, start, end, err);
-        if (n < 0) return;
+        kv_warp_find_rows<TPW>(p.c.cu, p.c.n_seq, tau0, ntok, n, start, end, err);
     } else {
         const int T = p.c.n_tok / p.c.n_seq;
-        n = tau / T;
+        n = tl < ntok ? (tau0 + tl) / T : -1;
         start = n * T;
         end = start + T;
     }
-    const int len = p.c.seq_lens[n];
-    if (end > p.c.n_tok || len < end - start || len > ((long long)p.c.max_pages << p.c.page_log2)) {
-        if (lane == 0) atomicOr(err, end > p.c.n_tok ? kErrSeqlens : kErrPages);
-        return;
+    long long base = -1;  // of token tl: where it goes
+    if (n >= 0) {
+        const int len = p.c.seq_lens[n];
+        if (end > p.c.n_tok || len < end - start || len > ((long long)p.c.max_pages << p.c.page_log2)) {
+            atomicOr(err, end > p.c.n_tok ? kErrSeqlens : kErrPages);
+        } else {
+            const int pos = len - (end - (tau0 + tl));
+            const int pg = kv_page(p.c, n, pos >> p.c.page_log2, err);
+            if (pg >= 0) base = ((long long)pg * hkv << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1));
+        }
     }
-    const int pos = len - (end - tau);
-    const int pg = kv_page(p.c, n, pos >> p.c.page_log2, err);
-    if (pg < 0) return;
-    const long long base = ((long long)pg * hkv << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1));
-    for (int h0 = 0; h0 < hkv; h0 += PB * RPP) {
-        if (h0 > 0) load(h0);
+    for (int r0 = 0; r0 < nr; r0 += PB * RPP) {
+        if (r0 > 0) load(r0);
 #pragma unroll
         for (int b = 0; b < PB; ++b) {
-            const int h = h0 + b * RPP + sub;
-            const long long row = h < hkv ? base + ((long long)h << p.c.page_log2) : -1;
+            const int r = r0 + b * RPP + sub, t = token_of(r);
+            const long long at = TPW == 1 ? base : __shfl_sync(0xffffffffu, base, t);
+            const long long row = r < nr && at >= 0 ? at + ((long long)(r - t * hkv) << p.c.page_log2) : -1;
 #pragma unroll
             for (int w = 0; w < 2; ++w) kv_store_row<TIn, D, E4M3>(p.c, w, row, col, u[w][b]);
         }
@@ -263,35 +291,45 @@ struct KvReadParams {
     void* y[2];  // dense keys and values, [n_tok][hkv][d]
 };
 
-// One warp per output token; a lane owns 8 channels of a head's row (16 bytes of bf16 output).
-template <typename TOut, int D, bool E4M3>
+// One warp per TPW output tokens; a lane owns 8 channels of a head's row (16 bytes of bf16 output).
+template <typename TOut, int D, bool E4M3, int TPW>
 __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_read_kernel(const KvReadParams p, unsigned* err) {
-    constexpr int LG = D / 8, RPP = 32 / LG, PB = 4;
+    constexpr int LG = D / 8, RPP = 32 / LG, PB = kKvBatch;
     const int lane = threadIdx.x & 31;
-    const int tau = blockIdx.x * kKvWarps + (threadIdx.x >> 5);
-    if (tau >= p.c.n_tok) return;
-    int start, end;
-    const int n = kv_warp_find(p.c.cu, p.c.n_seq, tau, start, end, err);
-    if (n < 0) return;
-    const int pos = tau - start;
-    if (end > p.c.n_tok || (pos >> p.c.page_log2) >= p.c.max_pages) {
-        if (lane == 0) atomicOr(err, end > p.c.n_tok ? kErrSeqlens : kErrPages);
-        return;
+    const int tau0 = (blockIdx.x * kKvWarps + (threadIdx.x >> 5)) * TPW, ntok = min(TPW, p.c.n_tok - tau0);
+    if (ntok <= 0) return;
+    const int tl = TPW == 1 ? 0 : lane;  // the token that this lane looks up
+    int n, start, end;
+    kv_warp_find_rows<TPW>(p.c.cu, p.c.n_seq, tau0, ntok, n, start, end, err);
+    long long base = -1;  // of token tl: where it lies in the cache
+    if (n >= 0) {
+        const int pos = tau0 + tl - start;
+        if (end > p.c.n_tok || (pos >> p.c.page_log2) >= p.c.max_pages) {
+            atomicOr(err, end > p.c.n_tok ? kErrSeqlens : kErrPages);
+        } else {
+            const int pg = kv_page(p.c, n, pos >> p.c.page_log2, err);
+            if (pg >= 0) base = ((long long)pg * p.c.hkv << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1));
+        }
     }
-    const int pg = kv_page(p.c, n, pos >> p.c.page_log2, err);
-    if (pg < 0) return;
-    const int hkv = p.c.hkv, sub = lane / LG, col = (lane % LG) * 8;
-    const long long base = ((long long)pg * hkv << p.c.page_log2) + (pos & ((1 << p.c.page_log2) - 1));
-    for (int h0 = 0; h0 < hkv; h0 += PB * RPP) {
+    // row r of the warp's ntok * hkv (head r mod hkv of token r / hkv) is row tau0 * hkv + r of the output
+    const int hkv = p.c.hkv, nr = ntok * hkv, sub = lane / LG, col = (lane % LG) * 8;
+    for (int r0 = 0; r0 < nr; r0 += PB * RPP) {
         uint4 u[2][PB];
         unsigned sc[2][PB];
+        bool have[PB];
 #pragma unroll
         for (int b = 0; b < PB; ++b) {
-            const int h = h0 + b * RPP + sub;
-            const long long row = base + ((long long)(h < hkv ? h : 0) << p.c.page_log2);
+            const int r = r0 + b * RPP + sub;
+            int t = 0;
+#pragma unroll
+            for (int i = 1; i < TPW; ++i) t += r >= i * hkv;
+            const long long at = TPW == 1 ? base : __shfl_sync(0xffffffffu, base, t);
+            const long long row = at + ((long long)(r - t * hkv) << p.c.page_log2);
+            have[b] = r < nr && at >= 0;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
                 const uint8_t* cache = static_cast<const uint8_t*>(w ? p.c.v_cache : p.c.k_cache);
+                if (!have[b]) continue;
                 if (E4M3) {
                     const uint2 c2 = *reinterpret_cast<const uint2*>(cache + row * D + col);
                     u[w][b] = make_uint4(c2.x, c2.y, 0, 0);
@@ -303,11 +341,11 @@ __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_read_kernel(const KvRead
         }
 #pragma unroll
         for (int b = 0; b < PB; ++b) {
-            const int h = h0 + b * RPP + sub;
-            if (h >= hkv) continue;
+            const int r = r0 + b * RPP + sub;
+            if (!have[b]) continue;
 #pragma unroll
             for (int w = 0; w < 2; ++w) {
-                TOut* dst = static_cast<TOut*>(p.y[w]) + ((long long)tau * hkv + h) * D + col;
+                TOut* dst = static_cast<TOut*>(p.y[w]) + ((long long)tau0 * hkv + r) * D + col;
                 float x[8];
                 if (E4M3) {
                     const float s = kv_scale_value(sc[w][b]);
