@@ -232,9 +232,9 @@ __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, T
         }
         return mine * p.c.hkv;
     };
-    long long W = 0, total;
-    for (int base = 0; base < N; base += per) {
-        block_scan<THREADS>(mine_of(base), total, sc->scan);
+    long long W = 0, total = 0, before = 0;
+    for (int base = 0; base < N; base += per) {  // once, up to 256 sequences
+        before = block_scan<THREADS>(mine_of(base), total, sc->scan);
         W += total;
     }
     const int grid = (int)min((long long)gridDim.x, W), cta = blockIdx.x;
@@ -242,7 +242,7 @@ __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, T
     const long long w0 = W * cta / grid, w1 = W * (cta + 1) / grid;
     long long seen = 0;
     for (int base = 0; base < N; base += per) {
-        const long long before = block_scan<THREADS>(mine_of(base), total, sc->scan);
+        if (N > per) before = block_scan<THREADS>(mine_of(base), total, sc->scan);
         if (seen + total <= w0) {
             seen += total;
             continue;
