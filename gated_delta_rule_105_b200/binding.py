@@ -700,6 +700,8 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, 
         _ints("cu_seqlens", cu_seqlens, n_seqs + 1)
     if o_dtype not in (torch.float32, torch.bfloat16):
         raise ValueError(f"o_dtype must be float32 or bfloat16, got {o_dtype}")
+    if not 0 <= window < 1 << 31:
+        raise ValueError(f"window must be in [0, 2^31), got {window}")
     device = q.device
     if o is None:
         o = torch.empty(n_tok, hq, d, dtype=o_dtype, device=device)

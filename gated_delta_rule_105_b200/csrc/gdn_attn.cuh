@@ -9,8 +9,8 @@
 // once in blocks of 128 or 256 (a unit).  All units of all items form one line, and each CTA takes an equal stretch of it
 // whatever the sequences' lengths are: the split depends on device-side lengths only, so a captured graph replays
 // with new lengths and nothing is read back.  A CTA ends up with whole items (written directly) and at most two parts
-// of items, its first and its last, whose unnormalised sums, maxima and denominators go to the workspace; the parts of an
-// item are then added in a fixed order.  The workspace is therefore a fixed size per CTA.
+// of items, its first and its last, whose unnormalised sums, maxima and denominators go to the workspace; a join kernel
+// adds the parts of an item in a fixed order.  The workspace is therefore a fixed size per CTA.
 #pragma once
 
 #include "gdn_kv.cuh"
@@ -40,12 +40,11 @@ struct AttnParams {
     int G, hq;
     int o_f32;
     int rows_lo, rows_hi;    // this kernel takes sequences with rows_lo < T G <= rows_hi
-    int* desc;               // decode: [grid][kDescInts], the split item that starts in this CTA, for the join kernel;
-                             // chunk: [grid][2] finished parts of that item's row tiles, 0 at the start
+    int* desc;               // [grid][kDescInts], the split item that starts in this CTA, for the join kernel
     float* part;             // [grid][2][R][d] partial sums (chunk: [grid][2][row tile][d / 4][128][4])
     float* ml;               // [grid][2][R][2] maximum (base 2) and denominator
 };
-// n (-1: none), KV head, first row, rows, slot of the first part, number of CTAs it spans
+// sequence (-1: none), KV head, first row, rows, slot of the first part, number of CTAs it spans, the first token's row
 constexpr int kDescInts = 8;
 
 // Units of one (KV head, row group) of a sequence, from the first unit of keys that any of its rows sees.
@@ -645,18 +644,23 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 }
 
 // ------------------------------------------------------------------------------------------ joining split items
-// Softmax parts combine like blocks do: a running maximum, sum and denominator, part after part.  An item of the decode
-// kernel has few rows and may have many parts (one long context shared out among all CTAs): a block takes one row, warp
-// w its parts w, w + 8, ..., and the warps' results combine the same way.  (The chunk kernel's parts are joined by the
-// warpgroup that finishes the item.)
+// Softmax parts combine like blocks do: by a common maximum, sums and denominators.  One launch joins the parts of both
+// kernels, the blocks of the decode kernel's items first.
+//
+// An item of the decode kernel has few rows and may have many parts (one long context shared out among all CTAs): a block
+// takes one row, warp w its parts w, w + 8, ..., with a running maximum, and the warps' results combine the same way.
 constexpr int kJoinWarps = 8;
-struct JoinParams {
+struct JoinArrays {
     const int* desc;
     const float* part;
     const float* ml;
+};
+struct JoinParams {
+    JoinArrays dec, tc;
     void* o;
     float* lse;
-    int rows;  // R of the attention kernel
+    int dec_blocks;
+    int rows;  // R of the decode kernel
     int G, hq, d, o_f32;
 };
 
@@ -674,13 +678,60 @@ struct JoinRow {
     }
 };
 
+// An item of the chunk kernel has 256 rows, in the layout [row tile][d / 4][128 rows][4]: a block takes 32 of them, a lane
+// one row, a warp NC groups of 4 channels.  The maximum over all parts comes first, then every part is added with its weight.
+constexpr int kJoinTileBlocks = 8;  // blocks of an item
+template <int NC>
+__device__ __forceinline__ void join_tile(const JoinParams& p, int block) {
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int c = block / kJoinTileBlocks, r = block % kJoinTileBlocks * 32 + lane;  // row of the item
+    const int4 d0 = reinterpret_cast<const int4*>(p.tc.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.tc.desc)[c * 2 + 1];
+    if (d0.x < 0 || r - lane >= d0.w) return;
+    const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
+    const bool there = r < rows;
+    auto slot = [&](int k) { return (c + k) * 2 + (k ? 0 : slot0); };
+    // (a part that has seen nothing of a row may not have written its sums)
+    auto ask = [&](int k) { return there ? reinterpret_cast<const float2*>(p.tc.ml)[slot(k) * 256 + r] : make_float2(-INFINITY, 0.f); };
+    float m = -INFINITY, l = 0.f;
+#pragma unroll 8
+    for (int k = 0; k < parts; ++k) m = fmaxf(m, ask(k).x);
+    float4 a[NC];
+#pragma unroll
+    for (int j = 0; j < NC; ++j) a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int k = 0; k < parts; ++k) {
+        const float2 x = ask(k);
+        const bool some = !(x.x == -INFINITY && x.y == 0.f);
+        const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - m);  // no maximum but a denominator: a NaN to pass on
+        const float4* src = reinterpret_cast<const float4*>(p.tc.part) + ((slot(k) * 2LL + (r >> 7)) * (8 * NC) + warp * NC) * 128 + (r & 127);
+        l += x.y * f;
+#pragma unroll
+        for (int j = 0; j < NC; ++j) {
+            const float4 v = some ? src[j * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
+            a[j].x = fmaf(v.x, f, a[j].x), a[j].y = fmaf(v.y, f, a[j].y), a[j].z = fmaf(v.z, f, a[j].z), a[j].w = fmaf(v.w, f, a[j].w);
+        }
+    }
+    if (!there) return;
+    const int row = d0.z + r, tok = row / p.G, gh = row - tok * p.G;
+    const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
+    const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll
+    for (int j = 0; j < NC; ++j) attn_store4(p.o, p.o_f32, at * p.d + (warp * NC + j) * 4, a[j], inv);
+    if (warp == 0 && p.lse) p.lse[at] = attn_lse(m, l);
+}
+
 __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const JoinParams p) {
     __shared__ float4 s_a[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
     cudaGridDependencySynchronize();
+    if ((int)blockIdx.x >= p.dec_blocks) {
+        if (p.d == 128) join_tile<4>(p, blockIdx.x - p.dec_blocks);
+        else join_tile<2>(p, blockIdx.x - p.dec_blocks);
+        return;
+    }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int c = blockIdx.x / p.rows, y = blockIdx.x - c * p.rows;
-    const int4 d0 = reinterpret_cast<const int4*>(p.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.desc)[c * 2 + 1];
+    const int4 d0 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2 + 1];
     if (d0.x < 0) return;
     const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
     const bool alone = parts <= kJoinWarps;  // few parts: a warp per row, and fewer blocks
@@ -694,8 +745,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const Jo
         ml = make_float2(-INFINITY, 0.f);
         if (i < parts) {
             const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * p.rows + r;
-            ml = *reinterpret_cast<const float2*>(p.ml + at * 2);
-            if (mine) v = *reinterpret_cast<const float4*>(p.part + at * p.d + 4 * lane);
+            ml = *reinterpret_cast<const float2*>(p.dec.ml + at * 2);
+            if (mine) v = *reinterpret_cast<const float4*>(p.dec.part + at * p.d + 4 * lane);
         }
     };
     JoinRow out{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};

@@ -132,11 +132,17 @@ static void launch_read(const KvReadParams& p, bool e4m3, unsigned* err, cudaStr
 
 // ---- attention
 // Which kernels a call launches, and its workspace: a function of the sizes that the host knows.  Sequences of up to
-// kDecMaxRows query rows per KV head belong to the decode kernel, longer ones to the chunk kernel.  Where every
-// sequence has as many tokens (no cu_seqlens) or there is but one, one kernel takes the call; a batch with no more
-// tokens than sequences is decoding, and the decode kernel takes all of it; else both run.  The decode kernel works on 8
-// rows at a time where that is enough (half the softmax and the accumulators), else on 16.
-constexpr int kDecMaxRows = 16;
+// dec_max_rows() query rows per KV head belong to the decode kernel, longer ones to the chunk kernel.  Where every
+// sequence has as many tokens (no cu_seqlens) or there is but one, one kernel takes the call; with no more tokens than
+// sequences it is taken for decoding of one token each; else both run.  The decode kernel works on 8 rows at a time where
+// that is enough (half the softmax and the accumulators), else on 16, reading an item's keys again for every 16.
+//
+// The limit, measured with one token a sequence and 8 | 16 | 32 | 48 heads per KV head, us:
+//   32 sequences of 8192, 4 KV heads, d = 128, bf16: decode  88 |  94 | 177 | 247, chunk 105 | 106 | 107 | 108
+//   the same, e4m3:                                  decode  64 |  67 | 119 | 169, chunk 140 | 141 | 142 | 142
+//   the same, d = 64, bf16:                          decode  52 |  53 |  91 | 128, chunk  91 |  92 |  92 |  92
+//   2 sequences of 4096, 2 KV heads, d = 128, bf16:  decode  10 |  13 |  14 |  17, chunk  33 |  34 |  35 |  35
+static int dec_max_rows(int d, bool e4m3) { return d * (e4m3 ? 1 : 2) <= 128 ? 32 : 16; }
 struct AttnArrays {
     int grid;  // 0: this kernel is not launched
     size_t desc, ml, part;
@@ -149,15 +155,16 @@ struct AttnPlan {
 };
 static AttnPlan attn_plan(int n_tok, int n_seqs, bool packed, int G, int d, bool e4m3) {
     AttnPlan a = {};
+    const int most = dec_max_rows(d, e4m3);
     a.limit = 0x7fffffff;
-    if (n_tok <= n_seqs) {
+    if (n_tok <= n_seqs && G <= most) {
         a.dec.grid = 1;
     } else if (n_seqs == 1 || !packed) {
-        if ((long long)(n_tok / n_seqs) * G <= kDecMaxRows) a.dec.grid = 1;
+        if ((long long)(n_tok / n_seqs) * G <= most) a.dec.grid = 1;
         else a.tc.grid = 1, a.limit = 0;
     } else {
         a.dec.grid = a.tc.grid = 1;
-        a.limit = kDecMaxRows;
+        a.limit = most;
     }
     auto place = [&](AttnArrays& r, int grid, int rows) {
         if (!r.grid) return;
@@ -192,10 +199,6 @@ static cudaError_t launch_decode(const AttnParams& p, int grid, unsigned* err, c
 template <int D, bool E4M3>
 static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, JoinParams& j, unsigned* err, cudaStream_t stream) {
     cudaError_t e;
-    if (plan.tc.grid) {  // the counts of finished parts
-        e = cudaMemsetAsync(ws + plan.tc.desc, 0, (size_t)plan.tc.grid * 2 * sizeof(int), stream);
-        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel: %s", cudaGetErrorString(e));
-    }
     if (plan.dec.grid) {
         use_arrays(p, plan.dec, ws);
         p.rows_lo = 0;
@@ -203,7 +206,7 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         e = plan.dec_rows == 8 ? launch_decode<D, E4M3, 8>(p, plan.dec.grid, err, stream)
                                : launch_decode<D, E4M3, 16>(p, plan.dec.grid, err, stream);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention decode kernel launch: %s", cudaGetErrorString(e));
-        j.desc = p.desc, j.part = p.part, j.ml = p.ml, j.rows = plan.dec_rows;
+        j.dec = {p.desc, p.part, p.ml};
     }
     if (plan.tc.grid) {
         use_arrays(p, plan.tc, ws);
@@ -222,11 +225,12 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
         // beside a decode kernel it takes the SMs that that one leaves (and ends after it, for the join)
         e = launch_after(kern, dim3(plan.tc.grid), dim3(L::THREADS), L::BYTES, stream, plan.dec.grid > 0, mk, mv, p, err);
         if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention chunk kernel launch: %s", cudaGetErrorString(e));
+        j.tc = {p.desc, p.part, p.ml};
     }
-    if (plan.dec.grid) {
-        e = launch_after(gdn_attn_join_kernel, dim3(plan.dec.grid * plan.dec_rows), dim3(kJoinWarps * 32), 0, stream, true, j);
-        if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
-    }
+    j.rows = plan.dec_rows;
+    j.dec_blocks = plan.dec.grid * plan.dec_rows;
+    e = launch_after(gdn_attn_join_kernel, dim3(j.dec_blocks + plan.tc.grid * kJoinTileBlocks), dim3(kJoinWarps * 32), 0, stream, true, j);
+    if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;
 }
 
@@ -379,7 +383,7 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     if (Hq < Hkv || Hq % Hkv != 0 || Hq / Hkv > 256)
         return fail(GDN_ERR_INVALID_ARG, "Hq must be 1 to 256 times Hkv (got %d, %d)", Hq, Hkv);
     if (o_dt != GDN_F32 && o_dt != GDN_BF16) return fail(GDN_ERR_UNSUPPORTED, "o is GDN_F32 or GDN_BF16 (got %d)", (int)o_dt);
-    if (!std::isfinite(scale)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite");
+    if (!std::isfinite(scale * kLog2e)) return fail(GDN_ERR_INVALID_ARG, "scale is not finite, or too large");
     if (window < 0) return fail(GDN_ERR_INVALID_ARG, "window must be >= 0 (got %d)", window);
     if ((long long)n_tok * (Hq / Hkv) > 0x7fffff00LL) return fail(GDN_ERR_UNSUPPORTED, "too many query rows");
     if (n_tok == 0) return GDN_OK;

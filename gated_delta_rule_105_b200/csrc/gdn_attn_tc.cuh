@@ -49,7 +49,6 @@ struct AttnTcCtl {
     // where this CTA's stretch starts
     long long W, w0, w1;
     int n, h, rt, x;
-    int ticket[2];
 };
 static_assert(sizeof(AttnTcCtl) <= 1024, "control block");
 // Used while the work is shared out, in Q's place.
@@ -209,12 +208,6 @@ struct TcSeg {
     }
 };
 
-// Workspace slot of part k of an item that starts at unit `from` in CTA `owner`: a CTA has two, for the part that its
-// stretch begins with and for another one at its end.
-__device__ __forceinline__ long long tc_slot(long long W, long long grid, int owner, int k, long long from) {
-    return (owner + k) * 2LL + (k == 0 && W * owner / grid != from ? 1 : 0);
-}
-
 // Shares out the units and finds this CTA's first segment; false: nothing to do.  All threads.
 template <int THREADS>
 __device__ __forceinline__ bool tc_schedule(const AttnParams& p, AttnTcCtl* c, TcScratch* sc, unsigned* err) {
@@ -293,7 +286,8 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
     AttnTcCtl* c = reinterpret_cast<AttnTcCtl*>(smem + L::OFF_CTL);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    cudaTriggerProgrammaticLaunchCompletion();
+    cudaTriggerProgrammaticLaunchCompletion();  // the join kernel may be brought up meanwhile
+    if (tid == 0) p.desc[blockIdx.x * kDescInts] = -1;
     if (!tc_schedule<L::THREADS>(p, c, reinterpret_cast<TcScratch*>(smem + L::OFF_Q), err)) {
         cudaGridDependencySynchronize();  // see the end of the kernel
         return;
@@ -654,81 +648,31 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             const bool whole = g.cnt == g.units;
             const long long at = (long long)(g.s.start + tok) * p.hq + g.h * p.G + gh;
             const float m2 = m == -INFINITY ? -INFINITY : m * cs;
-            // A part of an item is left in the workspace for whichever warpgroup finishes the item's last part; that one
-            // adds all parts in their order (so the result does not depend on which it is).
-            bool last = whole;
-            int owner = 0, parts = 1, mine = 0;
-            if (!whole) {
-                const long long grid = min((long long)gridDim.x, c->W), from = g.w - g.x;
-                owner = (int)(((from + 1) * grid + c->W - 1) / c->W) - 1;  // the CTA whose stretch holds the item's first tile
-                parts = (int)(((from + g.units) * grid + c->W - 1) / c->W) - owner;
-                mine = (int)blockIdx.x - owner;
-                const long long slot = tc_slot(c->W, grid, owner, mine, from);
+            // A part of an item goes to the workspace, for the join kernel.
+            const long long slot = blockIdx.x * 2LL + (g.w == c->w0 ? 0 : 1);
+            if (whole) {
+                if (there && p.lse) p.lse[at] = attn_lse(m2, l);
+            } else {
                 if (there) reinterpret_cast<float2*>(p.ml)[slot * kTcRows + i * kTcTile + r] = make_float2(m2, l);
-                if (b > a) {
-                    float4* dst = reinterpret_cast<float4*>(p.part) + (slot * 2 + i) * (D / 4) * kTcTile + r;
-#pragma unroll
-                    for (int q = 0; q < D / 32; ++q) {
-                        float o[32];
-                        tmem_ld32(to + q * 32, o);
-                        tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) dst[(q * 8 + e) * kTcTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
-                    }
+                if (i == 0 && r == 0 && g.x == 0) {  // the item starts here and ends in a later CTA
+                    const long long grid = min((long long)gridDim.x, c->W), end = g.w + g.units;
+                    int4* desc = reinterpret_cast<int4*>(p.desc) + blockIdx.x * 2;
+                    desc[0] = make_int4(g.n, g.h, g.rt * kTcRows, min(kTcRows, rows - g.rt * kTcRows));
+                    desc[1] = make_int4((int)(slot & 1), (int)((end * grid + c->W - 1) / c->W) - (int)blockIdx.x, g.s.start, 0);
                 }
-                named_bar_sync(1 + i, 128);
-                if (r == 0) {
-                    __threadfence();
-                    c->ticket[i] = atomicAdd(&p.desc[owner * 2 + i], 1);
-                    __threadfence();
-                }
-                named_bar_sync(1 + i, 128);
-                last = c->ticket[i] == parts - 1;
             }
-            if (last) {
-                float mm = m2, ll = l;
-                const long long grid = min((long long)gridDim.x, c->W), from = g.w - g.x;
-                if (!whole) {
-                    mm = -INFINITY, ll = 0.f;
-                    for (int k = 0; k < parts; ++k) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml) + tc_slot(c->W, grid, owner, k, from) * kTcRows + i * kTcTile + r);
-                        if (there && v.x > mm) mm = v.x;
-                    }
-                    for (int k = 0; k < parts; ++k) {
-                        const float2 v = __ldcg(reinterpret_cast<const float2*>(p.ml) + tc_slot(c->W, grid, owner, k, from) * kTcRows + i * kTcTile + r);
-                        ll += v.y * (v.x == -INFINITY ? 1.f : exp2f(v.x - mm));
-                    }
-                }
-                if (there && p.lse) p.lse[at] = attn_lse(mm, ll);
-                const float inv = ll == 0.f ? 0.f : 1.f / ll;
+            if (whole || b > a) {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
+                float4* dst = reinterpret_cast<float4*>(p.part) + (slot * 2 + i) * (D / 4) * kTcTile + r;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     float o[32];
-                    if (whole) {
-                        tmem_ld32(to + q * 32, o);
-                        tmem_wait_ld();
-                    } else {
+                    tmem_ld32(to + q * 32, o);
+                    tmem_wait_ld();
+                    if (!whole) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = 0.f;
-                        if (there) {
-                            for (int k = 0; k < parts; ++k) {
-                                const long long slot = tc_slot(c->W, grid, owner, k, from);
-                                const float2 ml = __ldcg(reinterpret_cast<const float2*>(p.ml) + slot * kTcRows + i * kTcTile + r);
-                                if (ml.x == -INFINITY && ml.y == 0.f) continue;  // nothing seen there: its sums may not be written
-                                const float f = ml.x == -INFINITY ? 1.f : exp2f(ml.x - mm);
-                                const float4* src = reinterpret_cast<const float4*>(p.part) + ((slot * 2 + i) * (D / 4) + q * 8) * kTcTile + r;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) {
-                                    const float4 v = __ldcg(src + e * kTcTile);
-                                    o[4 * e] = fmaf(v.x, f, o[4 * e]);
-                                    o[4 * e + 1] = fmaf(v.y, f, o[4 * e + 1]);
-                                    o[4 * e + 2] = fmaf(v.z, f, o[4 * e + 2]);
-                                    o[4 * e + 3] = fmaf(v.w, f, o[4 * e + 3]);
-                                }
-                            }
-                        }
-                    }
-                    if (there) {
+                        for (int e = 0; e < 8; ++e) dst[(q * 8 + e) * kTcTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);
+                    } else if (there) {
 #pragma unroll
                         for (int e = 0; e < 32; e += 4)
                             attn_store4(p.o, p.o_f32, at * D + q * 32 + e, make_float4(o[e], o[e + 1], o[e + 2], o[e + 3]), inv);

@@ -267,8 +267,8 @@ gdn_status gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, const 
  *             infinity or a NaN has byte 255 and reads back as NaN throughout.  The codes 0x7f and 0xff (e4m3's
  *             NaN) are never written and must not be put there by other means.
  * seq_lens int32 [n_seqs]: positions of each sequence in the cache, the call's new tokens among them.  New tokens are
- * packed: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 of the n_tok rows (int32 [n_seqs + 1], not
- * decreasing, within [0, n_tok]; rows behind cu_seqlens[n_seqs] belong to nobody and are neither read nor written), or,
+ * packed: sequence n's are rows cu_seqlens[n] .. cu_seqlens[n + 1] - 1 of the n_tok rows (int32 [n_seqs + 1], from 0, not
+ * decreasing, up to n_tok; rows behind cu_seqlens[n_seqs] belong to nobody and are neither read nor written), or,
  * with cu_seqlens NULL, n_tok / n_seqs rows each.  The last new token sits at position seq_lens[n] - 1.
  * Limits: d in {64, 128}; page_size in {16, 32, 64, 128}; n_seqs <= 65535; Hkv <= 1024; n_pages * Hkv * page_size <
  * 2^31; max_pages * page_size < 2^31 - 255.  Pointers 16-byte aligned.  Asynchronous on `stream`, no allocation; host

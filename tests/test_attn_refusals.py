@@ -142,3 +142,13 @@ def test_binding_refuses_cpu_tensors_and_wrong_shapes():
                  lambda: bd.add_rmsnorm_fwd(k, torch.ones(64), out_dtype=torch.float16)):
         with pytest.raises(ValueError):
             call()
+
+
+def test_scales_and_windows_out_of_range(lib):
+    assert attn(lib, scale=3e38) == 1  # times log2(e): no fp32 number
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(1, 4, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    for window in (-1, 1 << 31, (1 << 32) + 5):
+        with pytest.raises(ValueError, match="window"):
+            bd.paged_attn_fwd(q, kc, kc, bt, sl, window=window)

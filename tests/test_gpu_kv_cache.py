@@ -159,3 +159,105 @@ def test_bad_device_arguments_are_reported_and_skipped(what):
         g.kv_read(dev["kc"], dev["vc"], dev["table"], cu, n_rows)
         with pytest.raises(g.GdnError):
             g.check_error()
+
+
+def many(hkv, d, kind, lens, page=32, seed=0):
+    """A cache of random rows for sequences of the given lengths, on the device, and its block table."""
+    gen = torch.Generator().manual_seed(seed)
+    per = [-(-n // page) for n in lens]
+    pages = sum(per) + 1
+    table = torch.full((len(lens), max(per)), -1, dtype=torch.int32)
+    order, at = torch.randperm(pages, generator=gen).to(torch.int32), 0
+    for i, n in enumerate(per):
+        table[i, :n] = order[at:at + n]
+        at += n
+    shape = (pages, hkv, page, d)
+    if kind == "bf16":
+        c = [torch.randn(shape, generator=gen).bfloat16().cuda() for _ in range(2)] + [None, None]
+    else:
+        c = [torch.randint(0, 0x7f, shape, generator=gen, dtype=torch.uint8).view(torch.float8_e4m3fn).cuda() for _ in range(2)]
+        c += [torch.randint(120, 130, shape[:3], generator=gen, dtype=torch.uint8).cuda() for _ in range(2)]
+    return c, table.cuda(), torch.tensor([0, *np.cumsum(lens)], dtype=torch.int32).cuda()
+
+
+# heads and channels that put one, two and four tokens into a warp; lengths that end inside a warp's tokens, and none
+@pytest.mark.parametrize("hkv,d", [(1, 64), (3, 128), (4, 128), (5, 64), (16, 128)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_long_calls_read_what_is_there(hkv, d, kind):
+    g = lib()
+    lens = [0, 1501, 2, 0, 1000, 3, 1, 700]
+    (kc, vc, ks, vs), table, cu = many(hkv, d, kind, lens)
+    n, page = sum(lens), 32
+    out = [torch.full((n + 6, hkv, d), 9.0, device="cuda") for _ in range(2)]
+    g.kv_read(kc, vc, table, cu, n + 6, ks, vs, torch.float32, *out)
+    g.check_error()
+    for cache, scale, got in ((kc, ks, out[0]), (vc, vs, out[1])):
+        x = cache.float() if scale is None else cache.float() * torch.exp2(scale.float() - 127)[..., None]
+        for i, m in enumerate(lens):
+            pos = torch.arange(m, device="cuda")
+            want = x[table[i].long()[pos // page], :, pos % page]
+            assert torch.equal(got[int(cu[i]):int(cu[i]) + m], want), i
+        assert (got[n:] == 9).all()
+
+
+@pytest.mark.parametrize("hkv,d", [(1, 64), (3, 128), (4, 128), (5, 64), (16, 128)])
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_long_calls_write_what_short_ones_do(hkv, d, kind, dtype):
+    """Several tokens a warp against calls of few tokens, which the tests above hold against the definition."""
+    g = lib()
+    lens, new = [1501, 2, 40, 1003, 3, 1, 700], [1501, 0, 7, 999, 3, 1, 699]
+    a, table, _ = many(hkv, d, kind, lens)
+    b = [None if t is None else t.clone() for t in a]
+    cu = torch.tensor([0, *np.cumsum(new)], dtype=torch.int32)
+    n = int(cu[-1])
+    gen = torch.Generator().manual_seed(1)
+    k, v = (torch.randn(n + 5, hkv, d, generator=gen).to(dtype).cuda() for _ in range(2))
+    total = torch.tensor(lens, dtype=torch.int32).cuda()
+    g.kv_append(k, v, a[0], a[1], table, total, cu.cuda(), a[2], a[3])
+    for i, m in enumerate(new):
+        for lo in range(0, m, 500):  # the sequence's tokens in pieces
+            hi, at = min(m, lo + 500), int(cu[i])
+            g.kv_append(k[at + lo:at + hi], v[at + lo:at + hi], b[0], b[1], table[i:i + 1].clone(), total[i:i + 1] - (m - hi), None, b[2], b[3])
+    g.check_error()
+    for x, y in zip(a, b):
+        assert x is None or torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_long_uniform_call_and_bad_arguments_in_one():
+    g = lib()
+    lens = [800] * 4
+    a, table, cu = many(2, 64, "e4m3", lens)
+    b = [t.clone() for t in a]
+    gen = torch.Generator().manual_seed(2)
+    k, v = (torch.randn(2800, 2, 64, generator=gen).cuda() for _ in range(2))
+    total = torch.tensor(lens, dtype=torch.int32).cuda()
+    by = torch.arange(5, dtype=torch.int32, device="cuda") * 700
+    g.kv_append(k, v, a[0], a[1], table, total, None, a[2], a[3])
+    g.kv_append(k, v, b[0], b[1], table, total, by, b[2], b[3])
+    g.check_error()
+    for x, y in zip(a, b):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+    # a page outside the pool and a length below its tokens: those rows are skipped, the others written
+    bad, short = table.clone(), total.clone()
+    bad[1, 10], short[2] = 10 ** 6, 699
+    c = [torch.zeros_like(t) for t in a]
+    g.kv_append(k, v, c[0], c[1], bad, short, None, c[2], c[3])
+    with pytest.raises(g.GdnError):
+        g.check_error()
+    out = [torch.full((3200, 2, 64), 5.0, device="cuda") for _ in range(2)]
+    g.kv_read(c[0], c[1], bad, cu, 3200, c[2], c[3], torch.float32, *out)
+    with pytest.raises(g.GdnError):
+        g.check_error()
+    full = g.kv_read(a[0], a[1], table, cu, 3200, a[2], a[3], torch.float32)
+    g.check_error()
+    for got, want in zip(out, full):
+        for i in range(4):
+            s = slice(800 * i + 100, 800 * (i + 1))
+            if i == 2:
+                assert (got[s] == 0).all()
+            elif i == 1:
+                hole = slice(1120, 1152)  # page 10
+                assert (got[hole] == 5).all() and torch.equal(got[900:1120], want[900:1120]) and torch.equal(got[1152:1600], want[1152:1600])
+            else:
+                assert torch.equal(got[s], want[s])

@@ -300,3 +300,60 @@ def test_an_attention_layer_beside_a_mixer_layer():
     assert torch.allclose(out.double(), want, rtol=2.0 ** -6, atol=1e-6)
     tail = g.add_rmsnorm_fwd(out.reshape(n, -1)[:, :dm].contiguous(), w.cuda(), norm["s"])
     assert torch.isfinite(tail["y"].float()).all() and tail["s"].shape == (n, dm)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("hq,hkv,d,window", [(24, 1, 64, 0), (33, 1, 128, 0), (96, 2, 64, 40), (256, 1, 128, 0)])
+def test_many_heads_share_a_kv_head(kind, hq, hkv, d, window):
+    """One token a sequence with more query rows per KV head than the decode kernel takes at a time, or at all."""
+    c = Cache([300, 1, 129], [1] * 3, hkv, d, 32, kind, hq).fill()
+    o, lse, _ = check(c, hq, 4, window)
+    for i in range(3):  # the batch's other sequences do not matter
+        one = Cache([c.total[i]], [1], hkv, d, 32, kind, hq)
+        one.kc, one.vc, one.ks, one.vs, one.table, one.n_pages = c.kc, c.vc, c.ks, c.vs, c.table[i:i + 1], c.n_pages
+        q = queries(c, hq, 4)[i:i + 1]
+        a, la = call(one, q, window=window, scale=d ** -0.5)
+        eo, el = attn_excess(a, la, attn_reference(one, f64(q), d ** -0.5, window), one, window, torch.bfloat16)
+        assert eo <= 1.0 and el <= 1.0
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("total,new,hq,d,window", [([5000], [20], 16, 128, 0), ([5000], [35], 8, 64, 1000),
+                                                   ([2600, 7, 2000], [90, 1, 1], 4, 128, 0)])
+def test_short_chunks_over_long_contexts(kind, total, new, hq, d, window):
+    """Few items of many parts: every CTA has a tile or two, and the parts outnumber the items by far."""
+    c = Cache(total, new, 1, d, 64, kind, sum(new)).fill()
+    check(c, hq, 6, window)
+    check(c, hq, 6, window, torch.float32)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_captured_chunks_replay_with_other_sequences(kind):
+    """A mixed call captured once; replayed with other lengths and another share of the rows among the sequences."""
+    g = lib()
+    c = Cache([900, 700, 40], [200, 1, 39], 2, 64, 16, kind, 43).fill()
+    dev = c.cuda()
+    q = queries(c, 4, 2)
+    qd = q.cuda()
+    ws = torch.empty(g.paged_attn_workspace_bytes(240, 3, 4, 2, 64), dtype=torch.uint8, device="cuda")
+    o = torch.empty(240, 4, 64, dtype=torch.bfloat16, device="cuda")
+
+    def step():
+        return g.paged_attn_fwd(qd, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"], dev["ks"], dev["vs"],
+                                o=o, return_lse=True, workspace=ws)[1]
+
+    step()
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lse = step()
+    for total, new in (([900, 700, 40], [200, 1, 39]), ([300, 700, 5], [1, 238, 1]), ([900, 0, 1], [239, 0, 1]), ([7, 7, 9], [1, 2, 3])):
+        c.total, c.new, n = total, new, sum(new)
+        c.cu = torch.tensor([0, *np.cumsum(new)], dtype=torch.int32)
+        dev["cu"].copy_(c.cu)
+        dev["lens"].copy_(torch.tensor(total, dtype=torch.int32))
+        o.fill_(55)
+        graph.replay()
+        g.check_error()
+        eo, el = attn_excess(o[:n], lse[:n], attn_reference(c, f64(q), 0.125, 0), c, 0, torch.bfloat16)
+        assert eo <= 1.0 and el <= 1.0 and (o[n:] == 55).all()

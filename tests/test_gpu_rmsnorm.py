@@ -135,3 +135,32 @@ def test_gradients_agree_with_differences():
         size = float((got["dx"].double().cpu().abs() * (torch.as_tensor(dx).abs() + torch.as_tensor(dr).abs()).double()).sum()
                      + (got["dweight"].double().cpu().abs() * torch.as_tensor(dw).abs().double()).sum())
         assert abs(num - want) <= 2e-3 + 2.0 ** -11 * size
+
+
+@pytest.mark.parametrize("out", [None, torch.float8_e4m3fn])
+def test_forward_and_backward_captured_and_on_another_stream(out):
+    """One graph of both passes, replayed on new values beside an eager call on another stream."""
+    g = lib()
+    x, r, w = (t.cuda() for t in draw(700, 1024, torch.bfloat16, 11))
+    dy = draw(700, 1024, torch.bfloat16, 12)[0].cuda()
+    ws = torch.empty(g.add_rmsnorm_bwd_workspace_bytes(700, 1024), dtype=torch.uint8, device="cuda")
+
+    def both(x, ws):
+        o = g.add_rmsnorm_fwd(x, w, r, EPS, out, 128 if out else 0)
+        return {**o, **g.add_rmsnorm_bwd(dy, o["s"], w, o["rstd"], None, workspace=ws)}
+
+    both(x, ws)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = both(x, ws)
+    other = torch.cuda.Stream()
+    for seed in (21, 22, 23):
+        x.copy_(draw(700, 1024, torch.bfloat16, seed)[0])
+        torch.cuda.synchronize()
+        graph.replay()
+        with torch.cuda.stream(other):
+            want = both(x, None)
+        torch.cuda.synchronize()
+        for k, t in want.items():
+            assert t is None or torch.equal(t.view(torch.uint8), got[k].view(torch.uint8)), k
