@@ -659,8 +659,8 @@ struct JoinParams {
     JoinArrays dec, tc;
     void* o;
     float* lse;
-    int dec_blocks;
-    int rows;  // R of the decode kernel
+    int dec_blocks, dec_split;  // blocks for the decode kernel's items, and for each of them
+    int rows;                   // R of the decode kernel
     int G, hq, d, o_f32;
 };
 
@@ -730,46 +730,48 @@ __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const Jo
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x / p.rows, y = blockIdx.x - c * p.rows;
+    const int c = blockIdx.x / p.dec_split, y = blockIdx.x - c * p.dec_split;
     const int4 d0 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2 + 1];
     if (d0.x < 0) return;
     const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
-    const bool alone = parts <= kJoinWarps;  // few parts: a warp per row, and fewer blocks
-    const int r = alone ? y * kJoinWarps + warp : y, first = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
-    if (r >= rows) return;
+    const bool alone = parts <= kJoinWarps;  // few parts: a warp per row
+    const int first = alone ? 0 : warp, step = alone ? 1 : kJoinWarps;
     const bool mine = lane * 4 < p.d;
-    float4 v;
-    float2 ml;
-    auto ask = [&](int i) {
-        v = make_float4(0.f, 0.f, 0.f, 0.f);
-        ml = make_float2(-INFINITY, 0.f);
-        if (i < parts) {
-            const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * p.rows + r;
-            ml = *reinterpret_cast<const float2*>(p.dec.ml + at * 2);
-            if (mine) v = *reinterpret_cast<const float4*>(p.dec.part + at * p.d + 4 * lane);
-        }
-    };
-    JoinRow out{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
-    ask(first);
+    for (int r = alone ? y * kJoinWarps + warp : y; r < rows; r += alone ? p.dec_split * kJoinWarps : p.dec_split) {
+        float4 v;
+        float2 ml;
+        auto ask = [&](int i) {
+            v = make_float4(0.f, 0.f, 0.f, 0.f);
+            ml = make_float2(-INFINITY, 0.f);
+            if (i < parts) {
+                const long long at = ((long long)(c + i) * 2 + (i ? 0 : slot0)) * p.rows + r;
+                ml = *reinterpret_cast<const float2*>(p.dec.ml + at * 2);
+                if (mine) v = *reinterpret_cast<const float4*>(p.dec.part + at * p.d + 4 * lane);
+            }
+        };
+        JoinRow out{make_float4(0.f, 0.f, 0.f, 0.f), -INFINITY, 0.f};
+        ask(first);
 #pragma unroll 4
-    for (int i = first; i < parts; i += step) {
-        const float4 x = v;
-        const float2 xm = ml;
-        ask(i + step);
-        out.add(x, xm.x, xm.y);
-    }
-    if (!alone) {
-        s_a[warp][lane] = out.a;
-        if (lane == 0) s_ml[warp] = make_float2(out.m, out.l);
-        __syncthreads();
-        if (warp != 0) return;
+        for (int i = first; i < parts; i += step) {
+            const float4 x = v;
+            const float2 xm = ml;
+            ask(i + step);
+            out.add(x, xm.x, xm.y);
+        }
+        if (!alone) {
+            __syncthreads();  // the row before has been read
+            s_a[warp][lane] = out.a;
+            if (lane == 0) s_ml[warp] = make_float2(out.m, out.l);
+            __syncthreads();
+            if (warp != 0) continue;
 #pragma unroll
-        for (int w = 1; w < kJoinWarps; ++w) out.add(s_a[w][lane], s_ml[w].x, s_ml[w].y);
+            for (int w = 1; w < kJoinWarps; ++w) out.add(s_a[w][lane], s_ml[w].x, s_ml[w].y);
+        }
+        const int row = d0.z + r, tok = row / p.G, gh = row - tok * p.G;
+        const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
+        if (mine) attn_store4(p.o, p.o_f32, at * p.d + 4 * lane, out.a, out.l == 0.f ? 0.f : 1.f / out.l);
+        if (lane == 0 && p.lse) p.lse[at] = attn_lse(out.m, out.l);
     }
-    const int row = d0.z + r, tok = row / p.G, gh = row - tok * p.G;
-    const long long at = (long long)(start + tok) * p.hq + h * p.G + gh;
-    if (mine) attn_store4(p.o, p.o_f32, at * p.d + 4 * lane, out.a, out.l == 0.f ? 0.f : 1.f / out.l);
-    if (lane == 0 && p.lse) p.lse[at] = attn_lse(out.m, out.l);
 }
 
 }  // namespace gdn
