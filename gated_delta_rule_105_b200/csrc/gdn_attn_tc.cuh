@@ -186,8 +186,22 @@ struct TcSeg {
             rt = 0;
             if (++h == p.c.hkv) {
                 h = 0;
-                do s = tc_span(p, ++n, err);
-                while (s.T == 0);
+                // the next sequence of this kernel, 32 at a time: hundreds of decoding ones may lie between two chunks
+                unsigned some = 0;
+                SeqSpan t;
+                for (++n; n < p.c.n_seq; n += 32) {
+                    const int at = n + (threadIdx.x & 31);
+                    t.T = 0;
+                    if (at < p.c.n_seq) t = tc_span(p, at, err);
+                    some = __ballot_sync(0xffffffffu, t.T > 0);
+                    if (some) break;
+                }
+                if (!some) return false;  // (there is one)
+                const int l = __ffs(some) - 1;
+                n += l;
+                s.start = __shfl_sync(0xffffffffu, t.start, l);
+                s.T = __shfl_sync(0xffffffffu, t.T, l);
+                s.len = __shfl_sync(0xffffffffu, t.len, l);
                 rts = (s.T * p.G + kTcRows - 1) / kTcRows;
             }
         }

@@ -357,3 +357,12 @@ def test_captured_chunks_replay_with_other_sequences(kind):
         g.check_error()
         eo, el = attn_excess(o[:n], lse[:n], attn_reference(c, f64(q), 0.125, 0), c, 0, torch.bfloat16)
         assert eo <= 1.0 and el <= 1.0 and (o[n:] == 55).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+def test_work_far_apart_among_the_sequences(kind):
+    """Chunks with scores of decoding sequences between them, and decoding ones among many without a new token."""
+    total, new = [150] + [3] * 90 + [200] + [2] * 40 + [130, 260], [150] + [1] * 90 + [60] + [0] * 40 + [40, 1]
+    check(Cache(total, new, 2, 64, 32, kind, 61).fill(), 4, 3)
+    total, new = [5] + [1] * 100 + [300, 9] + [4] * 70 + [33], [1] + [0] * 100 + [1, 1] + [0] * 70 + [1]
+    check(Cache(total, new, 1, 128, 16, kind, 62).fill(), 4, 3)
