@@ -650,7 +650,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
 
 // ------------------------------------------------------------------------------------------ joining split items
 // Softmax parts combine like blocks do: by a common maximum, sums and denominators.  One launch joins the parts of both
-// kernels, the blocks of the decode kernel's items first.
+// kernels.
 //
 // An item of the decode kernel has few rows and may have many parts (one long context shared out among all CTAs): a block
 // takes one row, warp w its parts w, w + 8, ..., with a running maximum, and the warps' results combine the same way.
@@ -664,8 +664,8 @@ struct JoinParams {
     JoinArrays dec, tc;
     void* o;
     float* lse;
-    int dec_blocks, dec_split;  // blocks for the decode kernel's items, and for each of them
-    int rows;                   // R of the decode kernel
+    int tc_blocks, dec_split;  // blocks for the chunk kernel's items, and for each of the decode kernel's
+    int rows;                  // R of the decode kernel
     int G, hq, d, o_f32;
 };
 
@@ -684,7 +684,7 @@ struct JoinRow {
 };
 
 // An item of the chunk kernel has 256 rows, in the layout [row tile][d / 4][128 rows][4]: a block takes 32 of them, a lane
-// one row, a warp NC groups of 4 channels.  The maximum over all parts comes first, then every part is added with its weight.
+// one row, a warp NC groups of 4 channels, with a running maximum.  Everything of a part is asked for at once.
 constexpr int kJoinTileBlocks = 8;  // blocks of an item
 template <int NC>
 __device__ __forceinline__ void join_tile(const JoinParams& p, int block) {
@@ -694,27 +694,31 @@ __device__ __forceinline__ void join_tile(const JoinParams& p, int block) {
     if (d0.x < 0 || r - lane >= d0.w) return;
     const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;
     const bool there = r < rows;
-    auto slot = [&](int k) { return (c + k) * 2 + (k ? 0 : slot0); };
-    // (a part that has seen nothing of a row may not have written its sums)
-    auto ask = [&](int k) { return there ? reinterpret_cast<const float2*>(p.tc.ml)[slot(k) * 256 + r] : make_float2(-INFINITY, 0.f); };
+    constexpr int d4 = 8 * NC;  // groups of 4 channels
+    const int warp_at = ((r >> 7) * d4 + warp * NC) * 128 + (r & 127);
     float m = -INFINITY, l = 0.f;
-#pragma unroll 8
-    for (int k = 0; k < parts; ++k) m = fmaxf(m, ask(k).x);
     float4 a[NC];
 #pragma unroll
     for (int j = 0; j < NC; ++j) a[j] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int k = 0; k < parts; ++k) {
-        const float2 x = ask(k);
-        const bool some = !(x.x == -INFINITY && x.y == 0.f);
-        const float f = x.x == -INFINITY ? 1.f : exp2f(x.x - m);  // no maximum but a denominator: a NaN to pass on
-        const float4* src = reinterpret_cast<const float4*>(p.tc.part) + ((slot(k) * 2LL + (r >> 7)) * (8 * NC) + warp * NC) * 128 + (r & 127);
-        l += x.y * f;
+        const int slot = (c + k) * 2 + (k ? 0 : slot0);
+        const float2 x = reinterpret_cast<const float2*>(p.tc.ml)[slot * 256 + r];
+        float4 v[NC];
+#pragma unroll
+        for (int j = 0; j < NC; ++j) v[j] = reinterpret_cast<const float4*>(p.tc.part)[(long long)slot * (256 * d4) + warp_at + j * 128];
+        // a part that has seen nothing of a row may not have written its sums (what stands there is not used)
+        if (x.x == -INFINITY && x.y == 0.f) continue;
+        const float nm = fmaxf(m, x.x);
+        // (no maximum at all but a denominator: a NaN to pass on)
+        const float fa = m == -INFINITY ? (l == 0.f ? 0.f : 1.f) : exp2f(m - nm), fv = x.x == -INFINITY ? 1.f : exp2f(x.x - nm);
 #pragma unroll
         for (int j = 0; j < NC; ++j) {
-            const float4 v = some ? src[j * 128] : make_float4(0.f, 0.f, 0.f, 0.f);
-            a[j].x = fmaf(v.x, f, a[j].x), a[j].y = fmaf(v.y, f, a[j].y), a[j].z = fmaf(v.z, f, a[j].z), a[j].w = fmaf(v.w, f, a[j].w);
+            a[j].x = fmaf(v[j].x, fv, a[j].x * fa), a[j].y = fmaf(v[j].y, fv, a[j].y * fa);
+            a[j].z = fmaf(v[j].z, fv, a[j].z * fa), a[j].w = fmaf(v[j].w, fv, a[j].w * fa);
         }
+        l = fmaf(x.y, fv, l * fa);
+        m = nm;
     }
     if (!there) return;
     const int row = d0.z + r, tok = row / p.G, gh = row - tok * p.G;
@@ -729,13 +733,13 @@ __global__ void __launch_bounds__(kJoinWarps * 32) gdn_attn_join_kernel(const Jo
     __shared__ float4 s_a[kJoinWarps][32];
     __shared__ float2 s_ml[kJoinWarps];
     cudaGridDependencySynchronize();
-    if ((int)blockIdx.x >= p.dec_blocks) {
-        if (p.d == 128) join_tile<4>(p, blockIdx.x - p.dec_blocks);
-        else join_tile<2>(p, blockIdx.x - p.dec_blocks);
+    if ((int)blockIdx.x < p.tc_blocks) {  // the longer ones first
+        if (p.d == 128) join_tile<4>(p, blockIdx.x);
+        else join_tile<2>(p, blockIdx.x);
         return;
     }
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int c = blockIdx.x / p.dec_split, y = blockIdx.x - c * p.dec_split;
+    const int b = blockIdx.x - p.tc_blocks, c = b / p.dec_split, y = b - c * p.dec_split;
     const int4 d0 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2], d1 = reinterpret_cast<const int4*>(p.dec.desc)[c * 2 + 1];
     if (d0.x < 0) return;
     const int h = d0.y, rows = d0.w, slot0 = d1.x, parts = d1.y, start = d1.z;

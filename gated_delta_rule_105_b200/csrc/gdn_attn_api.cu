@@ -232,8 +232,8 @@ static gdn_status launch_attn(AttnParams p, const AttnPlan& plan, uint8_t* ws, J
     // One sequence of 4096, 16 rows: 17.8 us with a block per row, 18.0 with two, 25.4 with one; 64 sequences of up to
     // 16384: 145.0, 143.0 and 143.1; 23 sequences beside a chunk: 57.9, 55.3 and 54.7.
     j.dec_split = (long long)p.c.n_seq * p.c.hkv * kJoinWarps < plan.dec.grid ? plan.dec_rows : 2;
-    j.dec_blocks = plan.dec.grid * j.dec_split;
-    e = launch_after(gdn_attn_join_kernel, dim3(j.dec_blocks + plan.tc.grid * kJoinTileBlocks), dim3(kJoinWarps * 32), 0, stream, true, j);
+    j.tc_blocks = plan.tc.grid * kJoinTileBlocks;
+    e = launch_after(gdn_attn_join_kernel, dim3(j.tc_blocks + plan.dec.grid * j.dec_split), dim3(kJoinWarps * 32), 0, stream, true, j);
     if (e != cudaSuccess) return fail(GDN_ERR_CUDA, "attention join kernel launch: %s", cudaGetErrorString(e));
     return GDN_OK;
 }
