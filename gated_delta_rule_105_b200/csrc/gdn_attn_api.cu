@@ -56,8 +56,9 @@ static gdn_status check_cache(KvParams* c, const void* k_cache, const void* v_ca
         return fail(GDN_ERR_UNSUPPORTED, "the cache is GDN_BF16 or GDN_E4M3 (got %d)", (int)cache_dt);
     if ((long long)n_pages * Hkv * page_size > 0x7fffffffLL)
         return fail(GDN_ERR_UNSUPPORTED, "n_pages * Hkv * page_size must be below 2^31");
-    if ((long long)max_pages * page_size > 0x7fffff00LL)
-        return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size must be below 2^31 - 255");
+    // (the decode kernel looks up to four units of 384 keys past a sequence's end before it clamps the position)
+    if ((long long)max_pages * page_size > 0x7fffffffLL - 4095)
+        return fail(GDN_ERR_UNSUPPORTED, "max_pages * page_size must be at most 2^31 - 4096");
     gdn_status st = check_ptrs({k_cache, v_cache, table}, {k_scale, v_scale});
     if (st != GDN_OK) return st;
     if (cache_dt == GDN_E4M3 && (!k_scale || !v_scale))

@@ -271,7 +271,7 @@ gdn_status gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, const 
  * decreasing, up to n_tok; rows behind cu_seqlens[n_seqs] belong to nobody and are neither read nor written), or,
  * with cu_seqlens NULL, n_tok / n_seqs rows each.  The last new token sits at position seq_lens[n] - 1.
  * Limits: d in {64, 128}; page_size in {16, 32, 64, 128}; n_seqs <= 65535; Hkv <= 1024; n_pages * Hkv * page_size <
- * 2^31; max_pages * page_size < 2^31 - 255.  Pointers 16-byte aligned.  Asynchronous on `stream`, no allocation; host
+ * 2^31; max_pages * page_size <= 2^31 - 4096.  Pointers 16-byte aligned.  Asynchronous on `stream`, no allocation; host
  * checks first, as for gdn_chunk_fwd.  What only the device can see is reported by gdn_check_error as
  * GDN_ERR_DEVICE_ARG, without a fault: cu_seqlens out of order (the call's rows are then undefined); a sequence
  * length below its new tokens or beyond the block table (that sequence is skipped: nothing of it is written); a page

@@ -152,3 +152,12 @@ def test_scales_and_windows_out_of_range(lib):
     for window in (-1, 1 << 31, (1 << 32) + 5):
         with pytest.raises(ValueError, match="window"):
             bd.paged_attn_fwd(q, kc, kc, bt, sl, window=window)
+
+
+@pytest.mark.parametrize("page", [16, 128])
+def test_block_tables_whose_positions_would_pass_32_bits(lib, page):
+    """What the kernels add to a position before they clamp it must stay below 2^31."""
+    most = ((1 << 31) - 4096) // page
+    for call in (append, read, attn):
+        assert call(lib, page=page, max_pages=most + 1) == 2
+        assert "2^31 - 4096" in lib.gdn_last_error().decode()
