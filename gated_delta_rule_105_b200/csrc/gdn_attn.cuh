@@ -6,7 +6,7 @@
 //
 // Query heads share KV heads in groups of G, so the unit of work is an item: (sequence, KV head, group of query rows),
 // where row r of a (sequence, KV head) is new token r / G and head r mod G of the group.  Every item streams its keys
-// once in blocks of 128 or 256 (a unit).  All units of all items form one line, and each CTA takes an equal stretch of it
+// once in blocks of 128 to 384 (a unit).  All units of all items form one line, and each CTA takes an equal stretch of it
 // whatever the sequences' lengths are: the split depends on device-side lengths only, so a captured graph replays
 // with new lengths and nothing is read back.  A CTA ends up with whole items (written directly) and at most two parts
 // of items, its first and its last, whose unnormalised sums, maxima and denominators go to the workspace; a join kernel
