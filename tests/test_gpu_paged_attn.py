@@ -366,3 +366,71 @@ def test_work_far_apart_among_the_sequences(kind):
     check(Cache(total, new, 2, 64, 32, kind, 61).fill(), 4, 3)
     total, new = [5] + [1] * 100 + [300, 9] + [4] * 70 + [33], [1] + [0] * 100 + [1, 1] + [0] * 70 + [1]
     check(Cache(total, new, 1, 128, 16, kind, 62).fill(), 4, 3)
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float8_e4m3fn])
+def test_pages_behind_the_first_4_gb(kind):
+    """Pages at the end of a pool whose byte and element offsets pass 32 bits, against the same pages in a small pool."""
+    g = lib()
+    hkv, page, d, far = 2, 64, 128, (1 << 32) // (2 * 64 * 128) + 40  # pages: 2^32 elements and more
+    lens, new = [700, 130, 65], [1, 130, 40]
+    gen = torch.Generator().manual_seed(71)
+    k, v = (torch.randn(sum(lens), hkv, d, generator=gen).bfloat16().cuda() for _ in range(2))
+    q = torch.randn(sum(new), 8, d, generator=gen).bfloat16().cuda()
+    total = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    all_, cu = (torch.tensor([0, *np.cumsum(x)], dtype=torch.int32, device="cuda") for x in (lens, new))
+    near = torch.randperm(36, generator=gen).view(3, 12).to(torch.int32).cuda()
+    got = []
+    for pages, shift in ((36, 0), (far, far - 36)):
+        kc, vc = (torch.empty(pages, hkv, page, d, dtype=kind, device="cuda") for _ in range(2))
+        ks, vs = (None if kind is torch.bfloat16 else torch.empty(pages, hkv, page, dtype=torch.uint8, device="cuda") for _ in range(2))
+        for t in (kc, vc, ks, vs):  # nothing is left to chance in the places that no token takes
+            if t is not None:
+                t[shift:].view(torch.uint8).zero_()
+        table = near + shift
+        g.kv_append(k, v, kc, vc, table, total, all_, ks, vs)
+        got.append([*g.paged_attn_fwd(q, kc, vc, table, total, cu, ks, vs, return_lse=True),
+                    g.paged_attn_fwd(q[:3], kc, vc, table, total, None, ks, vs),
+                    *g.kv_read(kc, vc, table, all_, sum(lens), ks, vs)])
+        g.check_error()
+        del kc, vc, ks, vs
+    for a, b in zip(*got):
+        assert torch.equal(a, b)
+    if kind is torch.bfloat16:
+        assert torch.equal(got[1][3], k) and torch.equal(got[1][4], v)
+    torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new", [1, 40])
+def test_sequences_share_the_pages_of_a_prefix(kind, new):
+    c = Cache([200, 200, 150], [new] * 3, 2, 64, 32, kind, 81).fill()
+    for i in (1, 2):
+        c.table[i, :4] = c.table[0, :4]
+    check(c, 4, 2)
+    check(c, 4, 2, 70)
+
+
+def test_calls_without_tokens():
+    g = lib()
+    c = Cache([40, 9], [1, 1], 2, 64, 16, "e4m3", 82).fill()
+    dev = c.cuda()
+    before = {k: dev[k].view(torch.uint8).clone() for k in ("kc", "vc", "ks", "vs")}
+    none = torch.zeros(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    cu = torch.zeros(3, dtype=torch.int32, device="cuda")
+    for by in (cu, None):
+        g.kv_append(none, none, dev["kc"], dev["vc"], dev["table"], dev["lens"], by, dev["ks"], dev["vs"])
+        o, lse = g.paged_attn_fwd(none, dev["kc"], dev["vc"], dev["table"], dev["lens"], by, dev["ks"], dev["vs"], return_lse=True)
+        assert o.shape == (0, 2, 64) and lse.shape == (0, 2)
+    assert g.kv_read(dev["kc"], dev["vc"], dev["table"], cu, 0, dev["ks"], dev["vs"])[0].shape == (0, 2, 64)
+    # rows, but none that belongs to a sequence
+    q = torch.ones(5, 4, 64, dtype=torch.bfloat16, device="cuda")
+    o = torch.full((5, 4, 64), 3.0, dtype=torch.bfloat16, device="cuda")
+    g.paged_attn_fwd(q, dev["kc"], dev["vc"], dev["table"], dev["lens"], cu, dev["ks"], dev["vs"], o=o)
+    g.kv_append(q[:, :2].contiguous(), q[:, :2].contiguous(), dev["kc"], dev["vc"], dev["table"], dev["lens"], cu, dev["ks"], dev["vs"])
+    g.check_error()
+    assert (o == 3).all()
+    for k, t in before.items():
+        assert torch.equal(dev[k].view(torch.uint8), t)
+    n = g.add_rmsnorm_fwd(torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(128, device="cuda"))
+    assert n["y"].shape == (0, 128) and n["rstd"].shape == (0,)
