@@ -241,16 +241,20 @@ __global__ void __launch_bounds__(kKvWarps * 32) gdn_kv_append_kernel(const KvAp
         for (int i = 1; i < TPW; ++i) t += r >= i * hkv;
         return t;
     };
+    const uint4* src[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) src[w] = reinterpret_cast<const uint4*>(static_cast<const TIn*>(p.x[w]) + tau0 * p.stride[w]);
     uint4 u[2][PB];
     auto load = [&](int r0) {
 #pragma unroll
         for (int b = 0; b < PB; ++b) {
             const int r = r0 + b * RPP + sub, t = token_of(r);
 #pragma unroll
-            for (int w = 0; w < 2; ++w)
-                u[w][b] = r < nr ? *(reinterpret_cast<const uint4*>(static_cast<const TIn*>(p.x[w]) + (tau0 + t) * p.stride[w]) +
-                                     (r - t * hkv) * LG + col)
-                                 : make_uint4(0, 0, 0, 0);
+            for (int w = 0; w < 2; ++w) {
+                const uint4* at = src[w] + (r0 + b * RPP) * LG + lane;  // row r, as if the tokens' rows had no gaps
+                if (TPW > 1) at += t * (p.stride[w] * (int)sizeof(TIn) / 16 - hkv * LG);
+                u[w][b] = r < nr ? *at : make_uint4(0, 0, 0, 0);
+            }
         }
     };
     load(0);
