@@ -671,12 +671,10 @@ def paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d) -> int:
     return int(load_library().gdn_paged_attn_workspace_bytes(n_tok, n_seqs, Hq, Hkv, d))
 
 
-def _workspace_of(workspace, nbytes, device):
-    if workspace is None:
-        return torch.empty(nbytes, dtype=torch.uint8, device=device)
+def _check_workspace(workspace):
+    """The bytes of a workspace are counted by numel(): they must all be its own (an expanded tensor's are not)."""
     if workspace.dtype is not torch.uint8 or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous uint8 tensor")
-    return workspace
 
 
 def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, k_scale=None, v_scale=None, scale=None,
@@ -708,9 +706,10 @@ def paged_attn_fwd(q, k_cache, v_cache, block_table, seq_lens, cu_seqlens=None, 
     elif o.shape != shape or o.dtype is not o_dtype or not o.is_contiguous():
         raise ValueError(f"o must be a contiguous {o_dtype} {list(shape)}")
     lse = torch.empty(n_tok, hq, dtype=torch.float32, device=device) if return_lse else None
-    if workspace is None or workspace.dtype is not torch.uint8:
-        nbytes = paged_attn_workspace_bytes(n_tok, n_seqs, hq, hkv, d)
-        workspace = _workspace_of(workspace, nbytes, device)
+    if workspace is None:
+        workspace = torch.empty(paged_attn_workspace_bytes(n_tok, n_seqs, hq, hkv, d), dtype=torch.uint8, device=device)
+    else:
+        _check_workspace(workspace)
     dev = _device(q, k_cache, v_cache, k_scale, v_scale, block_table, seq_lens, cu_seqlens, o, workspace)
     _call(dev, load_library().gdn_paged_attn_fwd,
           q.data_ptr(), qs, k_cache.data_ptr(), v_cache.data_ptr(), _addr(k_scale), _addr(v_scale),
@@ -782,8 +781,10 @@ def add_rmsnorm_bwd(dy, s, weight, rstd, ds=None, dx=None, workspace=None):
     if dx is None:
         dx = torch.empty_like(s)
     dweight = torch.empty_like(weight)
-    if workspace is None or workspace.dtype is not torch.uint8:
-        workspace = _workspace_of(workspace, add_rmsnorm_bwd_workspace_bytes(rows, d), s.device)
+    if workspace is None:
+        workspace = torch.empty(add_rmsnorm_bwd_workspace_bytes(rows, d), dtype=torch.uint8, device=s.device)
+    else:
+        _check_workspace(workspace)
     _call(_device(s, dy, ds, dx, weight, rstd, workspace), load_library().gdn_add_rmsnorm_bwd,
           dy.data_ptr(), s.data_ptr(), weight.data_ptr(), rstd.data_ptr(), _addr(ds), dx.data_ptr(),
           dweight.data_ptr(), rows, d, _CODES[dt], workspace.data_ptr() or None, workspace.numel())

@@ -161,3 +161,20 @@ def test_block_tables_whose_positions_would_pass_32_bits(lib, page):
     for call in (append, read, attn):
         assert call(lib, page=page, max_pages=most + 1) == 2
         assert "2^31 - 4096" in lib.gdn_last_error().decode()
+
+
+def test_workspaces_whose_bytes_are_not_their_own(lib):
+    """numel() of an expanded or strided tensor is not what may be written from its address on."""
+    kc = torch.zeros(4, 2, 16, 64, dtype=torch.bfloat16)
+    bt, sl = torch.zeros(1, 4, dtype=torch.int32), torch.ones(1, dtype=torch.int32)
+    q = torch.zeros(1, 4, 64, dtype=torch.bfloat16)
+    s, w, rstd = torch.zeros(3, 64), torch.ones(64), torch.ones(3)
+    good = torch.empty(1 << 24, dtype=torch.uint8)
+    for bad in (torch.empty(1, dtype=torch.uint8).expand(1 << 24), good[::2], good.view(4096, 4096).T, good.view(torch.int8),
+                good.view(torch.float32)):
+        with pytest.raises(ValueError, match="contiguous uint8"):
+            bd.paged_attn_fwd(q, kc, kc, bt, sl, workspace=bad)
+        with pytest.raises(ValueError, match="contiguous uint8"):
+            bd.add_rmsnorm_bwd(s, s, w, rstd, workspace=bad)
+    with pytest.raises(ValueError, match="CUDA"):  # past this check, and refused for the tensors' device
+        bd.paged_attn_fwd(q, kc, kc, bt, sl, workspace=good)
