@@ -369,7 +369,11 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
         const uint32_t ring = sm100::smem_u32(smem) + warp * STAGES * Tr::STAGE;
         uint32_t st = ring, st_in = ring + (STAGES - 1) * Tr::STAGE;  // the stage in use and the one to fill
         auto advance = [&](uint32_t& at) { at = at == ring + (STAGES - 1) * Tr::STAGE ? ring : at + Tr::STAGE; };
-        look(k_begin);
+        // The first unit may begin before the first key that any row sees, where the block table may hold anything (pages that
+        // the window has passed): those rows, which the mask hides, are taken from that key's page.  Later units begin behind it.
+        const int first_key = p.window > 0 ? max(0, len - T + 1 - p.window) : 0;
+#pragma unroll
+        for (int kg = 0; kg < KG; ++kg) entry[kg] = table[max(position(k_begin, kg), first_key) >> p.c.page_log2];
 #pragma unroll
         for (int i = 0; i < STAGES - 1; ++i) {
             if (i < cnt) {

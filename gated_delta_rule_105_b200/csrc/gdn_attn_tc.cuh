@@ -171,6 +171,8 @@ struct TcSeg {
     static __device__ __forceinline__ int first_tile_of(const AttnParams& p, int pos) {
         return p.window > 0 ? max(0, pos - p.window + 1) / kTcTile : 0;
     }
+    // First key that any row of the item sees.
+    __device__ __forceinline__ int first_key(const AttnParams& p) const { return p.window > 0 ? max(0, pmin - p.window + 1) : 0; }
     __device__ __forceinline__ void start(const AttnParams& p, const AttnTcCtl* c, unsigned* err) {
         n = c->n, h = c->h, rt = c->rt, x = c->x, w = c->w0;
         s = tc_span(p, n, err);
@@ -354,10 +356,12 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             do {
                 const int t0 = g.tile0;
                 const int32_t* row = p.c.table + (long long)g.n * p.c.max_pages;
-                const int pages = (g.s.len + page - 1) >> p.c.page_log2;
-                auto look = [&](int tile) {  // this lane's page of a tile: -1 behind the sequence's end
+                // pages [first, pages) hold keys that the item sees; before them (the window has passed) and behind the
+                // sequence's end the table may hold anything
+                const int pages = (g.s.len + page - 1) >> p.c.page_log2, first = g.first_key(p) >> p.c.page_log2;
+                auto look = [&](int tile) {  // this lane's page of a tile: -1 where there is none to load
                     const int at = tile * npg + i;
-                    if (lane >= boxes || at >= pages) return -1;
+                    if (lane >= boxes || at < first || at >= pages) return -1;
                     const int pg = row[at];
                     if (pg >= 0 && pg < p.c.n_pages) return pg;
                     atomicOr(err, kErrPages);
@@ -714,7 +718,8 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             const int f0 = g.tile0;
             for (int j = 0; ok && j < g.cnt; ++j) {
                 const bool edge = TcSeg::edge(p, (f0 + j) * kTcTile, kTcTile, g.pmin, g.pmax);
-                const int valid = g.s.len - (f0 + j) * kTcTile;  // rows of the tile that are positions at all
+                // rows [unseen, valid) of the tile are keys that the item sees; the others' pages may not have been loaded
+                const int valid = g.s.len - (f0 + j) * kTcTile, unseen = g.first_key(p) - (f0 + j) * kTcTile;
 #pragma unroll 1
                 for (int kv = 0; kv < 2; ++kv) {
                     const int rs = fr % 2;
@@ -734,8 +739,8 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         // a value row that may be masked must be finite: one with the NaN scale is zeroed and marked
                         bool bad = false;
                         if (kv && edge) {
-                            bad = byte == kScaleNan && r < valid;
-                            if (byte == kScaleNan || r >= valid) byte = 0;
+                            bad = byte == kScaleNan && r < valid && r >= unseen;
+                            if (byte == kScaleNan || r >= valid || r < unseen) byte = 0;
                             const uint32_t hit = __ballot_sync(0xffffffffu, bad);
                             // the warp covers 32 / TPR neighbouring rows
                             uint32_t mark = 0;

@@ -258,8 +258,9 @@ gdn_status gdn_kda_chunk_bwd(const void* q, const void* k, const void* v, const 
  *
  * Paged key/value cache.  k_cache, v_cache [n_pages][Hkv][page_size][d] hold pages of page_size consecutive positions
  * for every KV head; block_table int32 [n_seqs][max_pages] names the page of positions [i page_size, (i + 1)
- * page_size) of each sequence (entries behind a sequence's last page are not read and may hold anything).  Pages
- * may be shared by sequences that only read them.  cache_dt:
+ * page_size) of each sequence (entries behind a sequence's last page are not read and may hold anything; nor does
+ * gdn_paged_attn_fwd with a window read those of pages before the first position that the call's tokens see, so that
+ * their pages may be given away).  Pages may be shared by sequences that only read them.  cache_dt:
  *   GDN_BF16  bf16 rows; k_scale and v_scale NULL.
  *   GDN_E4M3  8-bit codes and one scale byte per row, k_scale, v_scale uint8 [n_pages][Hkv][page_size]: a row's values
  *             are code * 2^(byte - 127), with the smallest exponent in [-117, 119] that keeps every code within 448

@@ -104,3 +104,14 @@ def attn_excess(o, lse, ref, c, window, o_dtype):
     bo = absv * (2.0 ** -8 + 2 * es[..., None] + 2.0 ** -21 + (2 * n + 64) * 2.0 ** -23) + U[o_dtype] * np.abs(ro)
     bl = es + 2.0 ** -22 + (n + 64) * 2.0 ** -23 + 4 * 2.0 ** -24 * np.abs(rl)
     return float(np.max(np.abs(f64(o) - ro) / bo)), float(np.max(np.abs(f64(lse) - rl) / bl))
+
+
+def attn_within(o, lse, ref, c, window, o_dtype):
+    """Every element within :func:`attn_excess`'s bound, without its quotients: a token that sees one key whose value has the
+    8-bit code 0 has output 0 and bound 0."""
+    ro, rl, absv, mass = ref
+    d, n = ro.shape[-1], min(max(c.total), window or max(c.total))
+    es = mass * (d * 2.0 ** -23 + 4 * 2.0 ** -24)
+    bo = absv * (2.0 ** -8 + 2 * es[..., None] + 2.0 ** -21 + (2 * n + 64) * 2.0 ** -23) + U[o_dtype] * np.abs(ro)
+    bl = es + 2.0 ** -22 + (n + 64) * 2.0 ** -23 + 4 * 2.0 ** -24 * np.abs(rl)
+    return bool(np.all(np.abs(f64(o) - ro) <= bo) and np.all(np.abs(f64(lse) - rl) <= bl))

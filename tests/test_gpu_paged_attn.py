@@ -4,7 +4,7 @@ import pytest
 import torch
 
 import oracle.attn as oa
-from attn_util import Cache, attn_excess, attn_reference, f64
+from attn_util import Cache, attn_excess, attn_reference, attn_within, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -434,3 +434,31 @@ def test_calls_without_tokens():
         assert torch.equal(dev[k].view(torch.uint8), t)
     n = g.add_rmsnorm_fwd(torch.zeros(0, 128, dtype=torch.bfloat16, device="cuda"), torch.ones(128, device="cuda"))
     assert n["y"].shape == (0, 128) and n["rstd"].shape == (0,)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("page", [16, 64, 128])
+@pytest.mark.parametrize("new,hq,d,window", [(1, 4, 64, 1), (1, 4, 128, 100), (3, 12, 64, 129), (2, 20, 128, 250), (90, 4, 128, 100),
+                                             (300, 2, 64, 65), (150, 6, 128, 1)])
+def test_pages_that_the_window_has_passed_may_be_gone(kind, page, new, hq, d, window):
+    """Block-table entries of pages that no token of the call sees: freed (any number), nothing is reported, and the
+    results are those of the full table to the bit."""
+    total = [900, 45 + new, 301 + new, 2 * new]
+    c = Cache(total, [new] * 4, 2, d, page, kind, page + new).fill()
+    q = queries(c, hq, 3)
+    want = call(c, q, window=window)
+    ref = attn_reference(c, f64(q), d ** -0.5, window)
+    assert attn_within(*want, ref, c, window, torch.bfloat16)
+    gone = 0
+    for i, (t, a) in enumerate(zip(c.total, c.new)):
+        first = max(0, t - a + 1 - window) // page
+        c.table[i, :first] = np.resize([-1, 1 << 30, -2 ** 31], first)
+        gone += first
+    assert gone > 0
+    dev = c.cuda()
+    for cu in (True, False):
+        o, lse = call(c, q, dev, cu=cu, window=window)  # (raises if the error word is set)
+        if cu:
+            assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        else:
+            assert attn_within(o, lse, ref, c, window, torch.bfloat16)
