@@ -172,6 +172,30 @@ __device__ __forceinline__ float scale_hi(uint32_t w) { return __uint_as_float((
 __device__ __forceinline__ bool bf16x2_nonfinite(uint32_t w) {
     return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
 }
+__device__ __forceinline__ bool bf16x8_nonfinite(const uint4& u) {
+    return bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w);
+}
+// The pair with 0 in the place of a NaN or an infinity.
+__device__ __forceinline__ uint32_t bf16x2_finite(uint32_t w) {
+    if ((w & 0x7f80u) == 0x7f80u) w &= 0xffff0000u;
+    if ((w & 0x7f800000u) == 0x7f800000u) w &= 0xffffu;
+    return w;
+}
+__device__ __forceinline__ uint4 bf16x8_finite(const uint4& u) {
+    return make_uint4(bf16x2_finite(u.x), bf16x2_finite(u.y), bf16x2_finite(u.z), bf16x2_finite(u.w));
+}
+// Adds what bf16x2_finite() took out of a pair of values to a row's sums of their channels.
+__device__ __forceinline__ void add_nonfinite(uint32_t w, float& lo, float& hi) {
+    if ((w & 0x7f80u) == 0x7f80u) lo += __uint_as_float(w << 16);
+    if ((w & 0x7f800000u) == 0x7f800000u) hi += __uint_as_float(w & 0xffff0000u);
+}
+// Row of the pool that holds position `key` of the sequence with this block table, KV head h (a bad page was reported when its
+// rows were asked for, and read as page 0).
+__device__ __forceinline__ long long attn_pool_row(const KvParams& c, const int32_t* table, int key, int h) {
+    int pg = table[key >> c.page_log2];
+    if ((unsigned)pg >= (unsigned)c.n_pages) pg = 0;
+    return (((long long)pg * c.hkv + h) << c.page_log2) + (key & ((1 << c.page_log2) - 1));
+}
 
 constexpr float kRescaleLog2 = 8.f;  // the running maximum follows only when it would be off by more than 2^8
 
@@ -383,6 +407,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
             copy_commit();
         }
 
+        bool taken_out = false;  // the same in all of the warp
         for (int x = 0; x < cnt; ++x) {
             const int k0 = k_begin + x * UNIT;
             copy_wait<STAGES - 2>();
@@ -516,29 +541,16 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     if (CH == 4 && (g & 1)) vr[i].x = vr[i].z, vr[i].y = vr[i].w;
                     if (CH == 16) vr2[i] = shared16(at + 128);
                 }
-                // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values there are taken out, and
-                // a row that does see such a key gets a NaN denominator (8-bit codes are always finite)
+                // ---- a masked key's V may hold anything, and 0 * NaN is NaN: non-finite values are taken out here, and added
+                // behind the last step to the rows that do see their key (8-bit codes are always finite)
                 if (!E4M3 && edge) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        bool bad = bf16x2_nonfinite(vr[i].x) || bf16x2_nonfinite(vr[i].y) || bf16x2_nonfinite(vr[i].z) ||
-                                   bf16x2_nonfinite(vr[i].w);
-                        if (CH == 16)
-                            bad = bad || bf16x2_nonfinite(vr2[i].x) || bf16x2_nonfinite(vr2[i].y) ||
-                                  bf16x2_nonfinite(vr2[i].z) || bf16x2_nonfinite(vr2[i].w);
+                        const bool bad = bf16x8_nonfinite(vr[i]) || (CH == 16 && bf16x8_nonfinite(vr2[i]));
                         if (!__any_sync(0xffffffffu, bad)) continue;
-                        unsigned any = bad;  // over the eight threads that hold this key
-                        any |= __shfl_xor_sync(0xffffffffu, any, 4);
-                        any |= __shfl_xor_sync(0xffffffffu, any, 8);
-                        any |= __shfl_xor_sync(0xffffffffu, any, 16);
-                        if (any) {
-                            vr[i] = make_uint4(0, 0, 0, 0);
-                            if (CH == 16) vr2[i] = make_uint4(0, 0, 0, 0);
-                            const int key = k0 + 16 * kg + 8 * (i >> 1) + 2 * t + (i & 1);
-#pragma unroll
-                            for (int r = 0; r < RS; ++r)
-                                if (key <= hi_[r] && key >= lo_[r]) l[r] = __int_as_float(0x7fc00000);
-                        }
+                        taken_out = true;
+                        vr[i] = bf16x8_finite(vr[i]);
+                        if (CH == 16) vr2[i] = bf16x8_finite(vr2[i]);
                     }
                 }
                 // ---- O^T += V^T P^T
@@ -570,6 +582,36 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 }
             }
             advance(st);
+        }
+        if (!E4M3 && taken_out) {
+            // The rare case: this warp's steps with masked keys once more, from the cache.  A non-finite value reaches its own
+            // channel of the rows that see its key, whatever their weight (and nothing else: not the denominators).
+            int hi[RS][2], lo[RS][2];  // of this thread's sums: rows 2t, 2t + 1 of each 8
+#pragma unroll
+            for (int r = 0; r < RS; ++r)
+#pragma unroll
+                for (int c = 0; c < 2; ++c) {
+                    hi[r][c] = __shfl_sync(0xffffffffu, hi_[r], 8 * t + 4 * c);
+                    lo[r][c] = __shfl_sync(0xffffffffu, lo_[r], 8 * t + 4 * c);
+                }
+#pragma unroll 1
+            for (int x = 0; x < cnt; ++x) {
+                const int k0 = k_begin + x * UNIT;
+                if (k0 >= full_lo && k0 + KS - 1 <= full_hi) continue;
+#pragma unroll 1
+                for (int key = max(k0, first_key); key < min(k0 + KS, len); ++key) {
+                    const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.c.v_cache) + attn_pool_row(p.c, table, key, h) * D;
+#pragma unroll
+                    for (int i = 0; i < MT; ++i) {
+                        const uint32_t w = *reinterpret_cast<const uint32_t*>(v + 64 * (i >> 2) + 8 * g + 2 * (i & 3));
+#pragma unroll
+                        for (int r = 0; r < RS; ++r) {
+                            if (key >= lo[r][0] && key <= hi[r][0]) add_nonfinite(w, o[r][i][0], o[r][i][2]);
+                            if (key >= lo[r][1] && key <= hi[r][1]) add_nonfinite(w, o[r][i][1], o[r][i][3]);
+                        }
+                    }
+                }
+            }
         }
         __syncthreads();  // every warp's ring is read: the join takes its place
 

@@ -20,8 +20,9 @@
 // the last P V and reads and writes its part of O itself.
 //
 // Masked keys.  A score that a row must not see is set to -inf before the maximum, so K may hold anything there.  For V a
-// weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, V rows with a NaN or an infinity
-// are zeroed in shared memory and marked, and a row that does see a marked key gets NaN.
+// weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, NaNs and infinities of V are zeroed in
+// shared memory (in 8 bits the rows with the NaN scale) and their keys marked; a row that does see a marked key gets them
+// at the end of its segment, each in its own channel, from the cache.
 #pragma once
 
 #include "gdn_attn.cuh"
@@ -50,6 +51,7 @@ struct AttnTcCtl {
     uint32_t tmem;
     volatile int abort_flag;
     uint32_t bad[3][4];  // marked keys of each V stage's tile
+    uint8_t saw[256];    // whether a row has seen a marked key (its own thread writes and reads it)
     // where this CTA's stretch starts
     long long W, w0, w1;
     int n, h, rt, x;
@@ -227,6 +229,36 @@ struct TcSeg {
         return k0 + n - 1 > lo || (p.window > 0 && k0 < hi - p.window + 1);
     }
 };
+
+// The rare case of a row at position `pos` that has seen marked keys in the segment: what was taken out of V goes to channels
+// [c0, c0 + 32) of its sums o, whatever the keys' weights.  A row of the 8-bit cache with the NaN scale is NaN throughout.
+template <int D, bool E4M3>
+__device__ __forceinline__ void add_marked(const AttnParams& p, const TcSeg& g, int pos, int c0, float (&o)[32]) {
+    if (E4M3) {
+#pragma unroll
+        for (int e = 0; e < 32; ++e) o[e] = __int_as_float(0x7fc00000);
+        return;
+    }
+    const int32_t* table = p.c.table + (long long)g.n * p.c.max_pages;
+    const int first = p.window > 0 ? max(0, pos - p.window + 1) : 0;
+#pragma unroll 1
+    for (int k0 = g.tile0 * kTcTile; k0 < (g.tile0 + g.cnt) * kTcTile; k0 += kTcTile) {
+        if (!TcSeg::edge(p, k0, kTcTile, g.pmin, g.pmax)) continue;
+#pragma unroll 1
+        for (int key = max(k0, first); key <= min(k0 + kTcTile - 1, pos); ++key) {
+            const uint4* v = reinterpret_cast<const uint4*>(static_cast<const __nv_bfloat16*>(p.c.v_cache) + attn_pool_row(p.c, table, key, g.h) * D + c0);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint4 u = v[e];
+                if (!bf16x8_nonfinite(u)) continue;
+                add_nonfinite(u.x, o[8 * e], o[8 * e + 1]);
+                add_nonfinite(u.y, o[8 * e + 2], o[8 * e + 3]);
+                add_nonfinite(u.z, o[8 * e + 4], o[8 * e + 5]);
+                add_nonfinite(u.w, o[8 * e + 6], o[8 * e + 7]);
+            }
+        }
+    }
+}
 
 // Shares out the units and finds this CTA's first segment; false: nothing to do.  All threads.
 template <int THREADS>
@@ -499,7 +531,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             int zero = 0;
             tc_warp_wait(&c->drain[i], 0, &zero, err);
         } else if (!E4M3) {
-            // ---- V rows that hold a NaN or an infinity, in tiles that are not wholly visible
+            // ---- NaNs and infinities of V, in tiles that are not wholly visible
             int cv = 0;
             bool ok = true;
             TcSeg g;
@@ -518,12 +550,13 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                             const int r = lane + 32 * rr;
                             bool bad = false;
                             for (int ch = 0; ch < D / 8; ++ch) {
-                                const uint4 u = *reinterpret_cast<const uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7));
-                                bad = bad || bf16x2_nonfinite(u.x) || bf16x2_nonfinite(u.y) || bf16x2_nonfinite(u.z) || bf16x2_nonfinite(u.w);
+                                uint4* at = reinterpret_cast<uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7));
+                                const uint4 u = *at;
+                                if (bf16x8_nonfinite(u)) {
+                                    *at = bf16x8_finite(u);
+                                    bad = true;
+                                }
                             }
-                            if (bad)
-                                for (int ch = 0; ch < D / 8; ++ch)
-                                    *reinterpret_cast<uint4*>(v + (ch >> 3) * L::HALF + sw128(r, ch & 7)) = make_uint4(0, 0, 0, 0);
                             const uint32_t m = __ballot_sync(0xffffffffu, bad);
                             if (lane == 0) c->bad[st][rr] = m;
                         }
@@ -566,6 +599,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
             int a, b, plo, phi;  // this row tile's steps and positions
             g.active(p, i, a, b, plo, phi);
+            c->saw[i * kTcTile + r] = 0;
             float m = -INFINITY, l = 0.f;
             for (int u = a; ok && u < b; ++u) {
                 const uint32_t tb = ts + (u & 1) * kTcStep;
@@ -624,7 +658,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     }
                 }
                 if (TcSeg::edge(p, (u >> 1) * kTcTile, kTcTile, g.pmin, g.pmax)) {
-                    // marked keys (see the head of the file): a row that sees one has no finite result
+                    // marked keys (see the head of the file)
                     const int cv = cv0 + (u >> 1) - g.tile0, st = cv % L::NV;
                     ok = tc_warp_wait(&c->v_ready[st], (cv / L::NV) & 1, ab, err);
                     if (!ok) break;
@@ -633,7 +667,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                         const int lo = clo - 32 * q, hi = chi - 32 * q;  // bits [lo, hi] of this word
                         if (hi < 0 || lo > 31) continue;
                         const uint32_t seen = (0xffffffffu >> (31 - min(hi, 31))) & (0xffffffffu << max(lo, 0));
-                        if (c->bad[st][(u & 1) * 2 + q] & seen) l = __int_as_float(0x7fc00000);
+                        if (c->bad[st][(u & 1) * 2 + q] & seen) c->saw[i * kTcTile + r] = 1;
                     }
                     __syncwarp();
                 }
@@ -685,12 +719,14 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
             if (whole || b > a) {
                 const float inv = l == 0.f ? 0.f : 1.f / l;
+                const bool saw = c->saw[i * kTcTile + r] != 0;
                 float4* dst = reinterpret_cast<float4*>(p.part) + (slot * 2 + i) * (D / 4) * kTcTile + r;
 #pragma unroll 1
                 for (int q = 0; q < D / 32; ++q) {
                     float o[32];
                     tmem_ld32(to + q * 32, o);
                     tmem_wait_ld();
+                    if (saw) add_marked<D, E4M3>(p, g, pos, q * 32, o);
                     if (!whole) {
 #pragma unroll
                         for (int e = 0; e < 8; ++e) dst[(q * 8 + e) * kTcTile] = make_float4(o[4 * e], o[4 * e + 1], o[4 * e + 2], o[4 * e + 3]);

@@ -300,10 +300,11 @@ gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* 
  *   o = sum_j p_j v_j / sum_j p_j,  p_j = exp(scale q . k_j),  over j <= i, and j > i - window when window > 0,
  * with the keys and values of KV head hq / (Hq / Hkv).  lse [n_tok][Hq] fp32 (NULL: not written) is the natural
  * logarithm of the denominator.  q [n_tok][Hq][d] bf16, token rows q_stride elements apart (>= Hq d, a multiple of 8);
- * o [n_tok][Hq][d] contiguous, bf16 or fp32.  Keys that a token does not see do not reach it, whatever they hold; a
- * token that sees a NaN, or an infinity in a value, gets non-finite outputs.  Scores, maxima, sums and outputs
- * are kept in fp32; the probabilities are rounded to bf16 for the product with V (over an 8-bit cache with V's scale
- * in them: value rows whose largest magnitude is below 2^-91 may lose bits there).
+ * o [n_tok][Hq][d] contiguous, bf16 or fp32.  Keys that a token does not see do not reach it, whatever they hold.  A NaN or
+ * an infinity in a value that a token sees makes that channel of its output non-finite (over an 8-bit cache every channel,
+ * as the row reads back), and neither its other channels nor lse; a token with a NaN or +infinity among its scores gets NaN in
+ * all of them.  Scores, maxima, sums and outputs are kept in fp32; the probabilities are rounded to bf16 for the product
+ * with V (over an 8-bit cache with V's scale in them: value rows whose largest magnitude is below 2^-91 may lose bits there).
  * Hq / Hkv up to 256.  Workspace: gdn_paged_attn_workspace_bytes() bytes, scratch as for gdn_chunk_fwd (not to be
  * shared by calls in flight at the same time).  The grid depends on the sizes given here alone, so a captured call can
  * be replayed after seq_lens, cu_seqlens, block_table and the cache changed.  Equal inputs give equal bits. */

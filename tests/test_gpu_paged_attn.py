@@ -462,3 +462,63 @@ def test_pages_that_the_window_has_passed_may_be_gone(kind, page, new, hq, d, wi
             assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         else:
             assert attn_within(o, lse, ref, c, window, torch.bfloat16)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,hq,d,window", [(1, 4, 64, 0), (1, 4, 128, 300), (3, 12, 64, 0), (4, 8, 128, 300), (90, 4, 128, 0),
+                                             (90, 4, 64, 300), (300, 2, 128, 0), (150, 6, 64, 333)])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -float("inf")])
+def test_a_bad_value_reaches_its_own_channel_only(kind, new, hq, d, window, value):
+    """A NaN or an infinity in one channel of a value: in the tokens that see it that channel is not finite (over 8 bits, where
+    the row is NaN throughout, every channel); other channels, other tokens and every lse are as without it, to the bit,
+    wherever the key lies -- in a tile that all rows of a chunk see, in one that some see, at the window's edge."""
+    L = 650
+    c = Cache([L, 40], [new, min(new, 40)], 2, d, 16, kind, seed=new).fill()
+    q = queries(c, hq, 2)
+    clean, clean_lse = call(c, q, window=window)
+    assert torch.isfinite(clean).all() and torch.isfinite(clean_lse).all()
+    first = max(0, L - new + 1 - window) if window else 0
+    for pos in sorted({first, first + 5, max(first, L - new - 200), max(first, L - new - 1), L - new + new // 2, L - 1}):
+        pg, r = c.table[0, pos // 16], pos % 16
+        if kind == "bf16":
+            was = c.vc[pg, :, r, 5].clone()
+            c.vc[pg, :, r, 5] = value
+        else:
+            was = c.vc.view(torch.uint8)[pg, :, r].clone(), c.vs[pg, :, r].clone()
+            c.put("v", pg, r, np.full((2, d), value))
+        o, lse = call(c, q, window=window)
+        assert torch.equal(lse, clean_lse), pos
+        for t in range(new):
+            own = L - new + t
+            if not (pos <= own and (not window or pos > own - window)):
+                assert torch.equal(o[t], clean[t]), (pos, t)
+            elif kind == "e4m3":
+                assert torch.isnan(o[t]).all(), (pos, t)
+            else:
+                assert torch.isnan(o[t, :, 5]).all() if np.isnan(value) else (o[t, :, 5] == value).all(), (pos, t)
+                assert torch.equal(o[t, :, :5], clean[t, :, :5]) and torch.equal(o[t, :, 6:], clean[t, :, 6:]), (pos, t)
+        assert torch.equal(o[new:], clean[new:])
+        if kind == "bf16":
+            c.vc[pg, :, r, 5] = was
+        else:
+            c.vc.view(torch.uint8)[pg, :, r], c.vs[pg, :, r] = was
+
+
+@pytest.mark.parametrize("new", [1, 60])
+@pytest.mark.parametrize("window", [0, 100])
+def test_opposite_infinities_among_the_values(new, window):
+    """+inf and -inf in one channel: NaN for the tokens that see both, an infinity for those that see one."""
+    L, hq, d = 400, 4, 64
+    c = Cache([L], [new], 1, d, 32, "bf16", 7).fill()
+    q = queries(c, hq, 3)
+    at = {L - new - 50: float("inf"), L - new // 2 - 1: -float("inf")}
+    for pos, value in at.items():
+        c.vc[c.table[0, pos // 32], :, pos % 32, 9] = value
+    o, lse = call(c, q, window=window)
+    assert torch.isfinite(lse).all()
+    for t in range(new):
+        own = L - new + t
+        want = sum(v for pos, v in at.items() if pos <= own and (not window or pos > own - window))
+        got = o[t, :, 9]
+        assert torch.isfinite(got).all() if want == 0 else torch.isnan(got).all() if np.isnan(want) else (got == want).all(), t
+        assert torch.isfinite(o[t, :, :9]).all() and torch.isfinite(o[t, :, 10:]).all()
