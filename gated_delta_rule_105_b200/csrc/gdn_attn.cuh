@@ -197,7 +197,10 @@ __device__ __forceinline__ long long attn_pool_row(const KvParams& c, const int3
     return (((long long)pg * c.hkv + h) << c.page_log2) + (key & ((1 << c.page_log2) - 1));
 }
 
-constexpr float kRescaleLog2 = 8.f;  // the running maximum follows only when it would be off by more than 2^8
+// The running maximum is lazy: sums are scaled down only when a row's maximum has grown by more than 2^8.  What is taken off
+// the scores is therefore 8 more than the maximum of that moment: no weight is ever above 1, and no finite value times a
+// weight leaves fp32's range.  (Behind such a step the largest weight is 2^-8, which costs neither fp32 nor bf16 a bit.)
+constexpr float kRescaleLog2 = 8.f;
 
 template <int D, bool E4M3, int R> struct DecTraits {
     static constexpr int RB = D * (E4M3 ? 1 : 2);          // bytes of a row
@@ -481,7 +484,7 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                 top[r] = -INFINITY;
 #pragma unroll
                 for (int kt = 0; kt < NT; ++kt) top[r] = fmaxf(top[r], fmaxf(s[kt][2 * r], s[kt][2 * r + 1]));
-                grow = grow || top[r] > m[r] + kRescaleLog2;
+                grow = grow || top[r] > m[r];
             }
             if (__any_sync(0xffffffffu, grow)) {
                 float f[RS];
@@ -490,10 +493,11 @@ gdn_attn_decode_kernel(const AttnParams p, unsigned* err) {
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 1));
                     top[r] = fmaxf(top[r], __shfl_xor_sync(0xffffffffu, top[r], 2));
                     f[r] = 1.f;
-                    if (top[r] > m[r] + kRescaleLog2) {  // each row by itself, whatever the others need
-                        f[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - top[r]);
+                    if (top[r] > m[r]) {  // each row by itself, whatever the others need
+                        const float up = top[r] + kRescaleLog2;
+                        f[r] = m[r] == -INFINITY ? 0.f : exp2f(m[r] - up);
                         l[r] *= f[r];
-                        m[r] = top[r];
+                        m[r] = up;
                     }
                 }
 #pragma unroll

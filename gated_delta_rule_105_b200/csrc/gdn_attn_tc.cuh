@@ -15,9 +15,9 @@
 //   warp 3        bf16 cache: looks for non-finite V rows in tiles that are not wholly visible (see below)
 //   warps 4 - 11  softmax: thread = row, the 64 scores of a step in registers, P back into the columns of S as bf16
 //   warps 12 - 15 8-bit cache: codes of a tile (bulk copies, one per page) to exact bf16 in the swizzled layout
-// Tensor memory: S/P of both tiles (2 x 2 x 64 columns) and O of both (2 x d).  The running maximum is lazy: O is scaled
-// down only when a row's maximum has grown by more than 2^8, which after the first steps is rare; then the warp waits for
-// the last P V and reads and writes its part of O itself.
+// Tensor memory: S/P of both tiles (2 x 2 x 64 columns) and O of both (2 x d).  The running maximum is lazy (kRescaleLog2):
+// that O is scaled down is rare after the first steps; then the warp waits for the last P V and reads and writes its part
+// of O itself.
 //
 // Masked keys.  A score that a row must not see is set to -inf before the maximum, so K may hold anything there.  For V a
 // weight of 0 is not enough, 0 * NaN is NaN: in tiles that some row does not see whole, NaNs and infinities of V are zeroed in
@@ -671,7 +671,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                     }
                     __syncwarp();
                 }
-                const float mc = m == -INFINITY ? 0.f : m * cs;
+                const float mc = m == -INFINITY ? 0.f : fmaf(m, cs, kRescaleLog2);
                 const float2 c2 = make_float2(cs, cs), mc2 = make_float2(-mc, -mc);
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
@@ -703,7 +703,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             tc_fence_after();
             const bool whole = g.cnt == g.units;
             const long long at = (long long)(g.s.start + tok) * p.hq + g.h * p.G + gh;
-            const float m2 = m == -INFINITY ? -INFINITY : m * cs;
+            const float m2 = m == -INFINITY ? -INFINITY : fmaf(m, cs, kRescaleLog2);
             // A part of an item goes to the workspace, for the join kernel.
             const long long slot = blockIdx.x * 2LL + (g.w == c->w0 ? 0 : 1);
             if (whole) {

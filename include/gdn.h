@@ -304,7 +304,9 @@ gdn_status gdn_kv_read(const void* k_cache, const void* v_cache, const uint8_t* 
  * an infinity in a value that a token sees makes that channel of its output non-finite (over an 8-bit cache every channel,
  * as the row reads back), and neither its other channels nor lse; a token with a NaN or +infinity among its scores gets NaN in
  * all of them.  Scores, maxima, sums and outputs are kept in fp32; the probabilities are rounded to bf16 for the product
- * with V (over an 8-bit cache with V's scale in them: value rows whose largest magnitude is below 2^-91 may lose bits there).
+ * with V (over an 8-bit cache with V's scale in them: value rows whose largest magnitude is below 2^-83 may lose bits there).
+ * Sums are taken with weights of at most 1 and divided once: they stay finite while the number of keys that a token sees
+ * times the largest |v| among them is below 2^127.
  * Hq / Hkv up to 256.  Workspace: gdn_paged_attn_workspace_bytes() bytes, scratch as for gdn_chunk_fwd (not to be
  * shared by calls in flight at the same time).  The grid depends on the sizes given here alone, so a captured call can
  * be replayed after seq_lens, cu_seqlens, block_table and the cache changed.  Equal inputs give equal bits. */

@@ -522,3 +522,43 @@ def test_opposite_infinities_among_the_values(new, window):
         got = o[t, :, 9]
         assert torch.isfinite(got).all() if want == 0 else torch.isnan(got).all() if np.isnan(want) else (got == want).all(), t
         assert torch.isfinite(o[t, :, :9]).all() and torch.isfinite(o[t, :, 10:]).all()
+
+
+@pytest.mark.parametrize("kind", [torch.bfloat16, torch.float8_e4m3fn])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("new,packed", [(1, True), (6, False), (40, True)])
+def test_large_values_under_rising_scores(kind, d, new, packed):
+    """Values close to fp32's largest number, and a key far along whose score is above the first one's by less than the running
+    maximum's lag (2^7.2): the weighted mean is finite.  Enough (sequence, head) items that CTAs walk along whole ones, and
+    a distance (768) that every unit of keys divides, so that one warp meets both keys."""
+    g = lib()
+    n, hkv, G, L, page = 8, 64, 2, 900, 64
+    gen = torch.Generator().manual_seed(d + new)
+    k = torch.zeros(L, hkv, d)
+    k[:, :, 0] = -40.0
+    k[3, :, 0], k[771, :, 0] = 0.0, 5.0
+    v = (1 + 0.8 * torch.rand(L, hkv, d, generator=gen)) * torch.sign(torch.randn(L, hkv, d, generator=gen)) * 2.0 ** 126
+    q = torch.zeros(n * new, hkv * G, d)
+    q[:, :, 0] = d ** 0.5 * (0.95 + 0.05 * torch.rand(n * new, hkv * G, generator=gen))
+    pages = -(-L // page)
+    kc, vc = (torch.zeros(pages, hkv, page, d, dtype=kind, device="cuda") for _ in range(2))
+    ks, vs = (None if kind is torch.bfloat16 else torch.zeros(pages, hkv, page, dtype=torch.uint8, device="cuda") for _ in range(2))
+    table = torch.randperm(pages, generator=gen).to(torch.int32).repeat(n, 1).cuda()
+    lens = torch.full((n,), L, dtype=torch.int32, device="cuda")
+    g.kv_append(k.bfloat16().cuda(), v.bfloat16().cuda(), kc, vc, table[:1].contiguous(), lens[:1], None, ks, vs)
+    q = q.bfloat16().cuda()
+    cu = torch.arange(0, n * new + 1, new, dtype=torch.int32, device="cuda") if packed else None
+    o, lse = g.paged_attn_fwd(q, kc, vc, table, lens, cu, ks, vs, o_dtype=torch.float32, return_lse=True)
+    kk, vv = g.kv_read(kc, vc, table[:1].contiguous(), torch.tensor([0, L], dtype=torch.int32, device="cuda"), L, ks, vs, torch.float32)
+    g.check_error()
+    # every new token lies behind both keys; the others' weights are below e^-38
+    s = torch.einsum("thgd,lhd->thgl", q.double().view(-1, hkv, G, d), kk.double()) * d ** -0.5
+    pos = (L - new + torch.arange(new, device="cuda")).repeat(n)
+    s.masked_fill_((torch.arange(L, device="cuda") > pos[:, None])[:, None, None], -float("inf"))
+    w = torch.softmax(s, -1)
+    want = torch.einsum("thgl,lhd->thgd", w, vv.double()).reshape(o.shape)
+    size = torch.einsum("thgl,lhd->thgd", w, vv.double().abs()).reshape(o.shape)
+    es = 40 * (d * 2.0 ** -23 + 4 * 2.0 ** -24)
+    assert torch.isfinite(o).all()
+    assert ((o.double() - want).abs() <= size * (2.0 ** -8 + 2 * es + 2.0 ** -21 + (2 * L + 64) * 2.0 ** -23) + 2.0 ** -24 * want.abs()).all()
+    assert ((lse.double() - torch.logsumexp(s, -1).reshape(lse.shape)).abs() <= es + 2.0 ** -22 + (L + 64) * 2.0 ** -23 + 40 * 2.0 ** -22).all()
