@@ -220,7 +220,7 @@ __global__ void __launch_bounds__(512) gdn_add_rmsnorm_kernel(const NormParams p
                 if (u < units) {
                     const float top = max_nan(amax, 1e-30f);
                     store_e4m3(static_cast<uint8_t*>(p.y) + base + 8 * u, s[i], 448.f / top);
-                    if ((u & 15) == 0) p.y_scale[row * (p.d / kNormGroup) + (u >> 4)] = top * (1.f / 448.f);
+                    if ((u & 15) == 0) p.y_scale[row * (p.d / kNormGroup) + (u >> 4)] = top / 448.f;
                 }
             }
         }
@@ -231,7 +231,7 @@ __global__ void __launch_bounds__(512) gdn_add_rmsnorm_kernel(const NormParams p
                 const int u = threadIdx.x + i * tpr;
                 if (u < units) store_e4m3(static_cast<uint8_t*>(p.y) + base + 8 * u, s[i], inv);
             }
-            if (threadIdx.x == 0) p.y_scale[row] = top * (1.f / 448.f);
+            if (threadIdx.x == 0) p.y_scale[row] = top / 448.f;
         }
         buf ^= 1;
     }

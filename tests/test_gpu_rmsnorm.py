@@ -177,3 +177,18 @@ def test_8_bit_scales_over_fp32_s_range(dt, group):
         gs = f64(got["scale"]).repeat(group or 256, -1)
         val = oa.e4m3_value(got["y"].cpu().view(torch.uint8).numpy()) * gs
         assert np.all(np.abs(val - y) <= np.maximum(2.0 ** -4 * np.abs(y), 2.0 ** -10 * gs) + 72 * u * np.abs(y))
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("group", [0, 128])
+@pytest.mark.parametrize("d", [256, 1024, 4096])
+def test_8_bit_scales_are_the_largest_output_over_448(dt, group, d):
+    """Given rstd, every step to a scale has one fp32 value: (s rstd) w, the largest magnitude, and its quotient by 448,
+    rounded once each.  The scales are those, to the bit."""
+    x, r, w = draw(200, d, dt, 17)
+    got = lib().add_rmsnorm_fwd(x.cuda(), w.cuda(), r.cuda(), EPS, torch.float8_e4m3fn, group)
+    s = x.float().numpy() + r.float().numpy()
+    y = (s * got["rstd"].cpu().numpy()[:, None]) * w.numpy()
+    assert y.dtype == np.float32
+    want = np.abs(y).reshape(200, -1, group or d).max(-1) / np.float32(448)
+    assert np.array_equal(got["scale"].cpu().numpy().reshape(want.shape), want)
