@@ -192,3 +192,45 @@ def test_8_bit_scales_are_the_largest_output_over_448(dt, group, d):
     assert y.dtype == np.float32
     want = np.abs(y).reshape(200, -1, group or d).max(-1) / np.float32(448)
     assert np.array_equal(got["scale"].cpu().numpy().reshape(want.shape), want)
+
+
+def test_gradients_agree_with_differences_where_the_mean_counts():
+    """Through the forward kernel, in fp32: differences of <dy, y> along the normed rows themselves (and along the weight), with
+    a dy that goes with them.  y does not change along its own row, so dx . xhat is all but 0, and only because the mean
+    term takes away rstd sum gw xhat, some 130 per row.
+
+    The bound: what the difference quotient of the fp64 definition misses of its derivative; the kernel's error in y, within
+    34 u |y| at either end of a step 2 h; and that of the gradients (see the head of the file)."""
+    g = lib()
+    h = 2.0 ** -4
+    x, r, w = draw(6, 384, torch.float32, 5)
+    W = f64(w)
+    S, R, _ = oa.add_rmsnorm(f64(x), f64(r), W, EPS)
+    xhat = torch.from_numpy(S * R[:, None]).float()
+    dy = xhat * w
+    DY, XH = f64(dy), f64(xhat)
+
+    def both(x, r, w):  # <dy, y> of the kernel and of the definition, and the kernel's outputs
+        o = g.add_rmsnorm_fwd(x.cuda(), w.cuda(), r.cuda(), EPS)
+        return float((f64(o["y"]) * DY).sum()), float((oa.add_rmsnorm(f64(x), f64(r), f64(w), EPS)[2] * DY).sum()), o
+
+    o = both(x, r, w)[2]
+    got = g.add_rmsnorm_bwd(dy.cuda(), o["s"], w.cuda(), o["rstd"])
+    dx, dw = oa.add_rmsnorm_grads(DY, S, W, R)
+    gw, xh, rs = DY * W, S * R[:, None], R[:, None]
+    m = np.mean(np.abs(gw * xh), -1, keepdims=True)
+    e_dx = (64 * u * (np.abs(rs * gw) + np.abs(rs * xh) * m) + 60 * u * np.abs(rs * xh) * m)  # with rstd's and s's own errors
+    e_dw = (6 + 20 + 34) * u * np.sum(np.abs(DY * xh), 0)
+    for a, b, c in ((xhat, 0, 0), (0, xhat, 0), (0, 0, w)):
+        (n1, d1, _), (n0, d0, _) = both(x + h * a, r + h * b, w + h * c), both(x - h * a, r - h * b, w - h * c)
+        num, num64 = (n1 - n0) / (2 * h), (d1 - d0) / (2 * h)
+        along = f64(torch.as_tensor(a)) + f64(torch.as_tensor(b))
+        exact = float((dx * along).sum() + (dw * f64(torch.as_tensor(c))).sum())
+        want = float((f64(got["dx"]) * along).sum() + (f64(got["dweight"]) * f64(torch.as_tensor(c))).sum())
+        size = float(np.sum(np.abs(DY * xh * W)) * (1 + h))
+        tol = abs(num64 - exact) + 34 * u * size / h + float(np.sum(e_dx * np.abs(along)) + np.sum(e_dw * np.abs(f64(torch.as_tensor(c)))))
+        assert tol < 1.0 and abs(num - want) <= tol, (num, want, tol)
+        if c is not w:  # gradients whose mean term is missing, halved, doubled or turned round are far outside
+            for factor in (0.0, 0.5, 2.0, -1.0):
+                wrong = rs * gw - factor * rs * xh * np.mean(gw * xh, -1, keepdims=True)
+                assert abs(num - float((wrong * along).sum())) > 100 * tol
