@@ -562,3 +562,70 @@ def test_large_values_under_rising_scores(kind, d, new, packed):
     assert torch.isfinite(o).all()
     assert ((o.double() - want).abs() <= size * (2.0 ** -8 + 2 * es + 2.0 ** -21 + (2 * L + 64) * 2.0 ** -23) + 2.0 ** -24 * want.abs()).all()
     assert ((lse.double() - torch.logsumexp(s, -1).reshape(lse.shape)).abs() <= es + 2.0 ** -22 + (L + 64) * 2.0 ** -23 + 40 * 2.0 ** -22).all()
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("n,chunks", [(257, {0: 40, 255: 150, 256: 60}), (300, {256: 40, 299: 90}), (700, {10: 33, 300: 140, 511: 50, 512: 50, 699: 70}),
+                                      (700, {690: 300}), (1030, {1024: 40, 1029: 9})])
+def test_chunks_far_along_many_sequences(kind, n, chunks):
+    """More sequences than either kernel looks over at a time, some of them with chunks, also in the last look only; one
+    token or none in the others."""
+    rng = np.random.default_rng(n)
+    new = [int(x) for x in rng.integers(0, 2, n)]
+    total = [int(x) for x in rng.integers(1, 6, n)]
+    if n == 700 and len(chunks) == 1:
+        new = [0] * n
+    for i, a in chunks.items():
+        new[i], total[i] = a, a + int(rng.integers(0, 200))
+    c = Cache(total, new, 2, 64, 16, kind, n).fill()
+    check(c, 8, 4)
+    check(c, 8, 4, 37)
+
+
+@pytest.mark.parametrize("kind", ["bf16", "e4m3"])
+@pytest.mark.parametrize("new,G,d,window", [(2, 5, 64, 0), (2, 8, 128, 0), (3, 4, 64, 50), (3, 3, 128, 0), (4, 8, 64, 0), (4, 3, 128, 90),
+                                            (2, 16, 64, 0), (4, 4, 128, 0), (4, 7, 64, 200)])
+def test_several_tokens_a_sequence_packed_and_not(kind, new, G, d, window):
+    """2 to 4 tokens of each sequence, 9 to 32 query rows per KV head: with cu_seqlens and without, several passes over the keys
+    or one."""
+    c = Cache([400, 129, new, 250, 61], [new] * 5, 2, d, 32, kind, new + G).fill()
+    q = queries(c, 2 * G, 5)
+    ref = attn_reference(c, f64(q), d ** -0.5, window)
+    for cu in (True, False):
+        for o_dtype in (torch.bfloat16, torch.float32):
+            o, lse = call(c, q, cu=cu, window=window, o_dtype=o_dtype)
+            assert attn_within(o, lse, ref, c, window, o_dtype), (cu, o_dtype)
+
+
+@pytest.mark.parametrize("variant,dv", [("gdn", 128), ("gdn", 256), ("gdn2", 128)])
+def test_chunks_beside_a_mixer_on_another_stream(variant, dv):
+    """The chunk kernel takes all of an SM's tensor memory, the mixer's kernels parts of it: calls of both on two streams
+    at once give what they give alone, to the bit."""
+    from gated_delta_rule_105_b200.inputs import generate
+    from parity_util import run_cuda
+    g = lib()
+    inp = generate(2, 1024, 8, 128, dv, "bf16", seed=5, variant=variant)
+    c = Cache([700, 300, 129], [130, 1, 60], 2, 128, 64, "bf16", 91).fill()
+    dev, q = c.cuda(), queries(c, 8, 2).cuda()
+    args = q, dev["kc"], dev["vc"], dev["table"], dev["lens"], dev["cu"]
+    ws = torch.empty(g.paged_attn_workspace_bytes(c.n_tok, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    want_mixer = run_cuda(inp, variant)
+    assert g.last_kernel() == "tc"
+    want = g.paged_attn_fwd(*args, return_lse=True)
+    g.check_error()
+    dev_inp = {k: v.cuda() if torch.is_tensor(v) else v for k, v in inp.items()}
+    one, two = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    mixer, attn = [], []
+    for _ in range(20):
+        with torch.cuda.stream(one):
+            mixer.append(run_cuda(dev_inp, variant))
+        with torch.cuda.stream(two):
+            for _ in range(4):
+                attn.append(g.paged_attn_fwd(*args, return_lse=True, workspace=ws))
+    torch.cuda.synchronize()
+    g.check_error()
+    for o, hT in mixer:
+        assert torch.equal(o, want_mixer[0]) and torch.equal(hT, want_mixer[1])
+    for o, lse in attn:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
