@@ -145,8 +145,8 @@ def last_kernel() -> str:
 
 
 def debug_stall(on: bool) -> None:
-    """Diagnostic of the device time-out path (``gdn_debug_stall``): while on, tensor-core GDN calls make a
-    pipeline wait run out; ``check_error`` then raises with status GDN_ERR_TIMEOUT."""
+    """Diagnostic of the device time-out path (``gdn_debug_stall``): while on, tensor-core GDN calls and paged attention over
+    chunks make a pipeline wait run out; ``check_error`` then raises with status GDN_ERR_TIMEOUT."""
     _raise_on(load_library().gdn_debug_stall(1 if on else 0))
 
 

@@ -53,6 +53,8 @@ gdn_status fail(gdn_status st, const char* fmt, ...) {
 
 void clear_error() { t_msg[0] = 0; }
 
+bool debug_stall() { return g_debug_stall.load() != 0; }
+
 // The error word's address on each device, looked up by the first call there (as for g_static_ws_addr).
 static std::atomic<unsigned*> g_err_word_addr[kMaxDevices];
 

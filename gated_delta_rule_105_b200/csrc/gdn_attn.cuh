@@ -39,6 +39,7 @@ struct AttnParams {
     int window;              // 0: none
     int G, hq;
     int o_f32;
+    int debug_stall;         // diagnostic (gdn_debug_stall): 0 in every ordinary call
     int rows_lo, rows_hi;    // this kernel takes sequences with rows_lo < T G <= rows_hi
     int* desc;               // [grid][kDescInts], the split item that starts in this CTA, for the join kernel
     float* part;             // [grid][2][R][d] partial sums (chunk: [grid][2][row tile][d / 4][128][4])

@@ -412,6 +412,7 @@ gdn_status gdn_paged_attn_fwd(const void* q, long long q_stride, const void* k_c
     p.G = Hq / Hkv;
     p.hq = Hq;
     p.o_f32 = o_dt == GDN_F32;
+    p.debug_stall = debug_stall();
     uint8_t* ws = static_cast<uint8_t*>(workspace);
     JoinParams j = {};
     j.o = o, j.lse = lse, j.G = p.G, j.hq = Hq, j.d = d, j.o_f32 = p.o_f32;

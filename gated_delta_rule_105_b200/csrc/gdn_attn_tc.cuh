@@ -48,6 +48,7 @@ template <int D, bool E4M3> struct AttnTc {
 struct AttnTcCtl {
     uint64_t q_full[2], k_full[3], k_empty[3], v_full[3], v_ready[3], v_empty[3], r_full[2], r_empty[2];
     uint64_t s_full[2][2], p_full[2][2], o_full[2][2], drain[2];  // [row tile][buffer of S]
+    uint64_t stall;  // diagnostic only: nothing ever arrives on it (gdn_debug_stall)
     uint32_t tmem;
     volatile int abort_flag;
     uint32_t bad[3][4];  // marked keys of each V stage's tile
@@ -81,13 +82,15 @@ __device__ __forceinline__ void tmem_ld16(uint32_t ta, uint32_t (&r)[16]) {
 }
 // gdn_sm100.cuh's bounded wait without its out-of-line part: a kernel that moves registers between its warpgroups
 // (setmaxnreg) cannot call functions.
-__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err) {
+constexpr long long kTcStallCycles = 2000000LL;  // of the diagnostic wait: about 1 ms
+__device__ __forceinline__ bool tc_wait(uint64_t* bar, uint32_t parity, volatile int* abort_flag, unsigned* err,
+                                        long long limit = sm100::kWaitLimitCycles) {
     if (sm100::mbar_try_wait(bar, parity)) return true;
     const long long t0 = clock64();
     while (true) {
         if (*abort_flag) return false;
         if (sm100::mbar_try_wait(bar, parity)) return true;
-        if (clock64() - t0 > sm100::kWaitLimitCycles) {
+        if (clock64() - t0 > limit) {
             *abort_flag = 1;
             atomicOr(err, kErrTimeout);
             return false;
@@ -354,6 +357,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
                 mbar_init(&c->o_full[i][j], 1);
             }
             mbar_init(&c->drain[i], 1);
+            if (i == 0) mbar_init(&c->stall, 1);
             mbar_init(&c->r_full[i], 1);
             mbar_init(&c->r_empty[i], 128);
         }
@@ -473,11 +477,14 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             };
             TcSeg g;
             g.start(p, c, err);
+            // Diagnostic: a wait that runs out.  It sets the error word and the abort flag, and this warp issues no MMA; every
+            // other role then leaves through its own bounded waits, behind which it drains what it issued.
+            if (p.debug_stall && i == 0) ok = __all_sync(0xffffffffu, tc_wait(&c->stall, 0, ab, err, kTcStallCycles));
             do {
                 const int u0 = g.tile0 * 2, tiles = g.cnt;
                 int a, b, plo, phi;
                 g.active(p, i, a, b, plo, phi);
-                ok = tc_warp_wait(&c->q_full[i], seg & 1, ab, err) && tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
+                ok = ok && tc_warp_wait(&c->q_full[i], seg & 1, ab, err) && tc_warp_wait(&c->k_full[ck % L::NK], (ck / L::NK) & 1, ab, err);
                 if (!ok) break;
                 tc_fence_after();
                 {
@@ -740,6 +747,7 @@ gdn_attn_chunk_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_con
             }
             tc_fence_before();  // O is free once the next Q (arrived after this) lets the issuer go on
         } while (ok && g.next(p, c, err));
+        tmem_wait_st();  // (a role that gave up may have left some of O's behind)
     } else {
         // ---- 8-bit cache: codes to bf16.  Eight (D = 64: four) threads share a row, 16 codes each.
         reg_dec<88>();

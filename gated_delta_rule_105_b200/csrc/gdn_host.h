@@ -20,6 +20,9 @@ void clear_error();
 // Device address of the current device's error word; nullptr with *st set when the look-up fails.
 unsigned* err_word_ptr(gdn_status* st);
 
+// Whether the device time-out diagnostic is on (gdn_debug_stall).
+bool debug_stall();
+
 // Allows `Kern` up to `bytes` of dynamic shared memory on the current device, once per device and process.
 template <auto Kern>
 cudaError_t allow_shared(int bytes) {
