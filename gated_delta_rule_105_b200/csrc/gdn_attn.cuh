@@ -109,10 +109,11 @@ __device__ __forceinline__ float attn_lse(float m, float l) {
 // channels of its key as its share of several k-steps (Q is loaded in the same order), and for V the keys of a step are
 // interleaved with byte permutes.  16-byte chunk c of row r lies at c ^ swizzle(r), which makes both reads free of bank
 // conflicts: K's (rows 2i and 2i + 1, chunks 0-3 or 4-7) and V's (rows 2t + const, chunks 2i and 2i + 1).
-// Measured, with the join: 64 sequences of up to 16384, 16 query and 4 KV heads x 128, e4m3: 143 to 147 us, 5.2 TB/s of
+// Measured, with the join: 64 sequences of up to 16384, 16 query and 4 KV heads x 128, e4m3: 139 to 147 us, 5.2 TB/s of
 // cache; one sequence of 4096, 2 KV heads, bf16: 17 us, of which the host's call is 11.  What is left is instructions: the
 // conversions of the 8-bit codes and the softmax of rows that the tile has and the item does not.  Two CTAs of 8 warps per
-// SM where the registers allow it (one of 12 for 16 rows): 148 us against 155 with one.
+// SM where the registers allow it (one of 12 for 16 rows): 148 us against 155 with one.  That is 128 registers a thread; for
+// e4m3 and d = 128 ptxas spills 60 bytes (stores; 96 of loads) there.
 //   S[q][key]: A = Q (16 rows), B = K; thread (g, t) = (lane / 4, lane % 4) gets rows g, g + 8 and keys 2t, 2t + 1.
 //   O^T[d][q]: A = V^T (16 channels x 16 keys), B = P^T, whose fragment is exactly S's: no shuffle in between.
 template <int CH>  // chunks of a row; 4: two rows share the 128 bytes of all banks

@@ -136,7 +136,10 @@ static void launch_read(const KvReadParams& p, bool e4m3, unsigned* err, cudaStr
 // dec_max_rows() query rows per KV head belong to the decode kernel, longer ones to the chunk kernel.  Where every
 // sequence has as many tokens (no cu_seqlens) or there is but one, one kernel takes the call; with no more tokens than
 // sequences it is taken for decoding of one token each; else both run.  The decode kernel works on 8 rows at a time where
-// that is enough (half the softmax and the accumulators), else on 16, reading an item's keys again for every 16.
+// that is enough (half the softmax and the accumulators), else on 16, reading an item's keys again for every 16.  Packed
+// calls choose those rows as for one token a sequence, since only the device knows the lengths: what has more rows than
+// that (several tokens a sequence; a chunk among slots that are mostly idle, n_tok <= n_seqs) reads its keys once per 8 or 16
+// rows.  Such calls are right, and not measured here.
 //
 // The limit, measured with one token a sequence and 8 | 16 | 32 | 48 heads per KV head, us:
 //   32 sequences of 8192, 4 KV heads, d = 128, bf16: decode  88 |  94 | 177 | 247, chunk 105 | 106 | 107 | 108

@@ -3,7 +3,7 @@
 // 128 keys.
 //
 // Bound by the tensor core on paper (4 d flops per row and key); measured over three sequences of up to 16384 positions
-// and 1000 new tokens, 16 query and 4 KV heads x 128, bf16: 327 to 335 us, 0.82 PFLOP/s.  A step of 64 keys takes a
+// and 1000 new tokens, 16 query and 4 KV heads x 128, bf16: 321 to 330 us, 0.83 PFLOP/s.  A step of 64 keys takes a
 // warpgroup 2150 cycles, of which its exponentials take 911 (512 if it had the SM's exp units to itself), rescaling and
 // maximum 470, reading S 290 and waiting for it 420; exp units and tensor core are both busy 45% of the time.
 //

@@ -8,9 +8,10 @@
 // 8-bit format.  A row x[d] (one token, one head) is stored as e4m3 codes and one scale byte b, value =
 // code * 2^(b - 127), with the smallest exponent e = b - 127 that keeps |x| <= 448 * 2^e.  A power of two costs
 // nothing in relative precision (e4m3 is itself a floating format), and it makes every stored value an exact bf16
-// number -- 4 significant bits, and e is kept within [-117, 119] so that none leaves bf16's normal range -- so the
-// attention over the 8-bit cache is the attention over its read-back, to the bit, and quantisation has no rounding
-// but the one to e4m3 (x * 2^-e is exact).  A row that holds an infinity or a NaN gets byte 255, the NaN scale,
+// number -- 4 significant bits, and e is kept within [-117, 119] so that none leaves bf16's normal range -- so that
+// attention over the 8-bit cache works on the same keys and values as over its read-back in a bf16 cache (results differ
+// by the order of sums, and by the decode kernel's f16 form of Q), and quantisation has no rounding but the one to e4m3
+// (x * 2^-e is exact).  A row that holds an infinity or a NaN gets byte 255, the NaN scale,
 // and reads back as NaN throughout: non-finite values are kept visible, and the codes themselves are always finite.
 #pragma once
 

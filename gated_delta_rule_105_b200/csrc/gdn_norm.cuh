@@ -11,7 +11,7 @@
 //
 // All of it is bound by HBM: every operand is read once and written once, a row stays in registers between its sum
 // and its output, and 8 channels per thread (16 bytes of bf16) are one access.  Measured at 16384 rows of 4096 bf16
-// channels: forward with 128-channel scales 80 us (5.9 TB/s), backward 100 us (5.4 TB/s); 48 rows of 2048: 15 us, of which
+// channels: forward with 128-channel scales 79 to 84 us (5.8 TB/s), backward 100 us (5.4 TB/s); 48 rows of 2048: 15 us, of which
 // the host's call is 11.
 #pragma once
 
