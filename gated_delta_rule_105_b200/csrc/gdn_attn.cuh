@@ -16,7 +16,7 @@
 #include "gdn_kv.cuh"
 
 // gdn_sm100.cuh defines one out-of-line function; declared static first, it stays local to this translation unit (the
-// library's other one has its own).
+// library's other one has its own).  It is not marked there: bench.py's record of DRAM traffic goes by that header's text.
 namespace gdn {
 namespace sm100 {
 static __device__ __noinline__ bool mbar_wait_slow(uint64_t* bar, uint32_t parity, volatile int* abort_flag,
